@@ -79,6 +79,9 @@ typedef int32_t cg_status;
 #define CG_FLAG_BAD_SYMBOL 0x8 /* encode input symbol >= A */
 #define CG_FLAG_TIMEOUT 0x10   /* a bounded wait for another CTA ran out;
                                   offsets and packed bytes are not valid */
+#define CG_FLAG_BATCH 0x20     /* 4-bit cache: a page id outside the pool, a
+                                  kv_len that the table cannot hold, or a
+                                  sequence of more than max_rows rows */
 
 /* Limits of this implementation. */
 #define CG_MAX_LAYERS 1024
@@ -400,6 +403,114 @@ cg_status cg_compress_chunk_ex(const uint16_t *k, const uint16_t *v,
                                uint32_t *len, uint64_t *off, void *workspace,
                                uint64_t workspace_bytes, int32_t *status,
                                cudaStream_t stream);
+
+/* ---- 4-bit paged cache ---------------------------------------------------
+ * A cache to serve from once a context has been restored (or is being
+ * written token by token): K and V held in 4 bits in pages of a pool, written
+ * as tokens arrive, read back, and attended over in place.
+ *
+ * Z  A group is `group` consecutive channels of one (layer, token, KV head) of
+ *    K or of V. m = its least value, M = its greatest; s = (M - m) / 15 in
+ *    binary32, rounded to seven significant bits (half up), then to the
+ *    cache's 16-bit type; c = rint((x - m) / s) in binary32 with every
+ *    operation rounded on its own, clamped to [0, 15] (0 when s = 0). Stored: c,
+ *    and the pair (s, m) in the cache's type, which is the inputs' type.
+ *    A group with an infinity or a NaN, or whose M - m passes the largest
+ *    binary32, is stored as s = m = NaN, c = 0, and sets CG_FLAG_NONFINITE.
+ *    (Seven bits of s times four bits of c are exact in binary16, so products
+ *    with the codes on the tensor cores round nothing.)
+ * U  Value: x^ = s c + m in binary32 (one rounding); a read rounds it to the
+ *    output type, values past its largest becoming its largest.
+ * N  Attention of query row i (position p of its sequence) and query head h
+ *    over KV head h / (Hq / H): keys j <= p (and j > p - window when window >
+ *    0), S_j = scale * sum_d q_d x^_jd, out = sum_j softmax(S)_j v^_j, lse =
+ *    ln sum_j exp S_j. A row that sees no key gets out = 0, lse = -inf.
+ *
+ * Pool bytes: [L][pages][H][page_tokens / 16] records of 16 tokens, each
+ * 16*D + 128*(D/group) bytes:
+ *    K codes  16 token rows of D/2 bytes: four chunks t of D/32 words w
+ *             (32-bit, little-endian); nibble 4*el + 2*jj + eh of word w holds
+ *             channel 16*(2*w + jj) + 4*t + 2*eh + el;
+ *    V codes  two halves of 8 tokens, each [g 8][pair 4][parity 2][D/16
+ *             bytes]: token 2*pair + parity of the half, channels g*D/8 + 0, 1,
+ *             ... from the low nibble up;
+ *    params   K then V: [16 tokens][D/group][s, m], 16 bits each.
+ * (The orders in which a warp's matrix fragments take them: a fragment is one
+ * contiguous load a lane.) The content of slots that no sequence holds is
+ * never looked at.
+ */
+#define CG_DT_F16 0
+#define CG_DT_BF16 1
+
+typedef struct cg_kv4_shape {
+    int32_t L;           /* layers, <= CG_MAX_LAYERS */
+    int32_t pages;       /* pages of the pool */
+    int32_t page_tokens; /* a multiple of 16, <= 1024 */
+    int32_t H;           /* KV heads, <= 1024 */
+    int32_t D;           /* channels a head: 64, 128 or 256 */
+    int32_t group;       /* 32, 64 or 128, <= D */
+    int32_t dtype;       /* CG_DT_*: inputs, outputs of attention, s and m */
+} cg_kv4_shape;
+
+/* The rows of one call. Sequence b has kv_len[b] tokens, token j of it on page
+ * table[b][j / page_tokens] at j % page_tokens; its rows of this call,
+ * start[b] .. start[b + 1] - 1, are its last ones (the last has position
+ * kv_len[b] - 1; kv_len counts them). start == NULL: one row a sequence, rows
+ * == B. Device arrays; the host numbers bound them: rows past `rows` and the
+ * rows of a sequence with more than max_rows are left out (CG_FLAG_BATCH). Rows
+ * that no sequence has (start[B] < rows) are neither read nor written. A row
+ * at a negative position (more rows than tokens), on a page id outside
+ * [0, pages) or past the table is not stored, reads as 0, and is seen by no
+ * query; each but the first sets CG_FLAG_BATCH. */
+typedef struct cg_kv4_batch {
+    int32_t B;
+    int32_t max_pages; /* width of the table */
+    int32_t rows;
+    int32_t max_rows; /* most rows of one sequence */
+    const int32_t *table;
+    const int32_t *kv_len;
+    const int32_t *start;
+} cg_kv4_batch;
+
+/* Bytes of the pool, and of one of its records; 0 for an invalid shape. */
+uint64_t cg_kv4_pool_bytes(const cg_kv4_shape *shape);
+uint64_t cg_kv4_record_bytes(const cg_kv4_shape *shape);
+
+/* Z: the batch's rows of layers [layer, layer + nlayers) into their slots. k,
+ * v: [nlayers][rows][H*D] of the cache's type, a row's channels contiguous,
+ * rows k_row_stride and layers k_layer_stride elements apart (v likewise): views
+ * of a fused projection's output do. pool 16-byte aligned. */
+cg_status cg_kv4_write(uint8_t *pool, const cg_kv4_shape *shape,
+                       const cg_kv4_batch *batch, int32_t layer,
+                       int32_t nlayers, const void *k, const void *v,
+                       int64_t k_row_stride, int64_t v_row_stride,
+                       int64_t k_layer_stride, int64_t v_layer_stride,
+                       int32_t *status, cudaStream_t stream);
+
+/* U: the batch's rows back out of their slots, as binary32 (out_f32 != 0) or
+ * the cache's type; out_k, out_v [nlayers][rows][H*D], both with these
+ * strides. */
+cg_status cg_kv4_read(const uint8_t *pool, const cg_kv4_shape *shape,
+                      const cg_kv4_batch *batch, int32_t layer,
+                      int32_t nlayers, int32_t out_f32, void *out_k,
+                      void *out_v, int64_t row_stride, int64_t layer_stride,
+                      int32_t *status, cudaStream_t stream);
+
+/* N over one layer: q [rows][Hq][D] (rows q_row_stride elements apart) -> out
+ * [rows][Hq][D] (out_row_stride), and lse [rows][Hq] binary32 unless NULL. Hq is a
+ * multiple of H. window <= 0: none. The rows' own tokens have to be in the pool
+ * already. workspace: cg_kv4_attention_workspace_bytes(), 256-byte aligned,
+ * any content; calls that overlap on the GPU need one each. */
+uint64_t cg_kv4_attention_workspace_bytes(const cg_kv4_shape *shape,
+                                          const cg_kv4_batch *batch,
+                                          int32_t Hq);
+cg_status cg_kv4_attention(const uint8_t *pool, const cg_kv4_shape *shape,
+                           const cg_kv4_batch *batch, int32_t layer,
+                           int32_t Hq, const void *q, int64_t q_row_stride,
+                           float scale, int32_t window, void *out,
+                           int64_t out_row_stride, float *lse,
+                           void *workspace, uint64_t workspace_bytes,
+                           int32_t *status, cudaStream_t stream);
 
 /* Library version string ("cachegen-gb300 <formats> <options> <build>"). */
 const char *cg_version(void);

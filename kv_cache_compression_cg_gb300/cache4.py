@@ -1,0 +1,209 @@
+"""The 4-bit paged cache for PyTorch tensors: a pool of pages that K and V are
+quantised into as they are written, read back from, and attended over
+(`cg_kv4_*` of include/cachegen.h, where the formulas and the layout stand).
+
+    cache = Cache4(L=32, pages=4096, page_tokens=64, H=8, D=128)
+    batch = Batch4(table, kv_len)                 # one new token a sequence
+    cache.write(k, v, batch, layer)               # k, v: [rows, H, D]
+    out = cache.attend(q, batch, layer)           # q: [rows, Hq, D]
+
+A prompt's chunk, several rows a sequence, is the same with `start`; a prefix
+restored by `codec.Codec` goes into all layers at once with `write_layers`.
+"""
+from __future__ import annotations
+
+import ctypes as C
+
+import torch
+
+from . import capi
+
+__all__ = ["Cache4", "Batch4"]
+
+_DTYPES = {torch.float16: capi.CG_DT_F16, torch.bfloat16: capi.CG_DT_BF16}
+
+
+def _stream(stream: torch.cuda.Stream | None) -> int:
+    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+
+
+class Batch4:
+    """Where the rows of a call belong.
+
+    table: int32 [B, max_pages], page ids of each sequence in order; kv_len:
+    int32 [B], tokens of each sequence, its rows of this call included; start:
+    int32 [B + 1], row offsets (None: one row a sequence). A sequence's rows are its
+    last ones. All on the GPU. rows and max_rows, the number of rows and the most that
+    one sequence has, are the host's (with start, rows is required; max_rows
+    defaults to rows). A batch can be kept over calls: what the arrays hold is read by
+    each call, on its stream.
+    """
+
+    def __init__(self, table: torch.Tensor, kv_len: torch.Tensor, start: torch.Tensor | None = None,
+                 rows: int | None = None, max_rows: int | None = None):
+        for name, t in (("table", table), ("kv_len", kv_len), ("start", start)):
+            if t is None:
+                continue
+            if t.dtype != torch.int32:
+                raise TypeError(f"{name} must be torch.int32")
+            if not t.is_cuda or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous CUDA tensor")
+        if table.dim() != 2 or kv_len.dim() != 1 or kv_len.shape[0] != table.shape[0]:
+            raise ValueError("table must be [B, max_pages] and kv_len [B]")
+        B = table.shape[0]
+        if start is None:
+            if rows not in (None, B):
+                raise ValueError("without start every sequence has one row")
+            rows, max_rows = B, 1
+        else:
+            if start.shape != (B + 1,):
+                raise ValueError("start must be [B + 1]")
+            if rows is None:
+                raise ValueError("rows (the number of rows, known to the host) is required with start")
+            max_rows = rows if max_rows is None else max_rows
+            if rows < 0 or max_rows < 0:
+                raise ValueError("rows and max_rows must not be negative")
+        if len({t.device for t in (table, kv_len, start) if t is not None}) != 1:
+            raise ValueError("table, kv_len and start must be on one device")
+        self.table, self.kv_len, self.start = table, kv_len, start
+        self.rows, self.max_rows = int(rows), int(max_rows)
+        self._c = capi.cg_kv4_batch(B, table.shape[1], self.rows, self.max_rows, table.data_ptr(), kv_len.data_ptr(),
+                                    None if start is None else start.data_ptr())
+        self._ref = C.byref(self._c)
+
+
+class Cache4:
+    """Pool of `pages` pages of `page_tokens` tokens for L layers of H KV heads
+    of D channels, quantised by groups of `group` channels. dtype (float16 or
+    bfloat16) is the type of K, V, queries and outputs. `pool`: bytes to use
+    in place of new ones (uint8, contiguous, pool_bytes() of them).
+
+    `status` (int32 [1]) collects the CG_FLAG_* bits of all calls; zero it to start anew.
+    """
+
+    def __init__(self, L: int, pages: int, page_tokens: int, H: int, D: int, group: int = 64,
+                 dtype: torch.dtype = torch.float16, device: str | torch.device = "cuda",
+                 pool: torch.Tensor | None = None):
+        if dtype not in _DTYPES:
+            raise TypeError("dtype must be torch.float16 or torch.bfloat16")
+        self.L, self.pages, self.page_tokens, self.H, self.D, self.group, self.dtype = L, pages, page_tokens, H, D, group, dtype
+        self._c = capi.cg_kv4_shape(L, pages, page_tokens, H, D, group, _DTYPES[dtype])
+        self._ref = C.byref(self._c)
+        self._lib = capi.load()
+        self.nbytes = int(self._lib.cg_kv4_pool_bytes(self._ref))
+        if self.nbytes == 0:
+            raise ValueError("invalid shape for the cache: D is 64, 128 or 256, group 32, 64 or 128 and at most D, "
+                             "page_tokens a multiple of 16 up to 1024")
+        self.record_bytes = int(self._lib.cg_kv4_record_bytes(self._ref))
+        if pool is None:
+            pool = torch.zeros((L, pages, H, page_tokens // 16, self.record_bytes), dtype=torch.uint8, device=device)
+        elif pool.dtype != torch.uint8 or not pool.is_cuda or not pool.is_contiguous() or pool.numel() != self.nbytes:
+            raise ValueError(f"pool must be {self.nbytes} contiguous uint8 on the GPU")
+        elif pool.data_ptr() % 16:
+            raise ValueError("pool must be 16-byte aligned")
+        self.pool = pool
+        self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        self._pool, self._status = pool.data_ptr(), self.status.data_ptr()
+
+    def _kv(self, name, t, batch, layers):
+        """Strides (row, layer) of t: [rows, H, D] or [rows, H*D], with a dimension of layers before where there are several."""
+        if t.dtype != self.dtype:
+            raise TypeError(f"{name} must be {self.dtype}")
+        if t.device != self.pool.device:
+            raise ValueError(f"{name} must be on the cache's device")
+        HD = self.H * self.D
+        lead = () if layers is None else (layers,)
+        if t.shape == (*lead, batch.rows, HD):
+            ok = t.stride(-1) == 1
+        elif t.shape == (*lead, batch.rows, self.H, self.D):
+            ok = t.stride(-1) == 1 and (t.stride(-2) == self.D or self.H == 1)
+        else:
+            ok = False
+        if not ok:
+            raise ValueError(f"{name} must be {[*lead, batch.rows, HD]} (or with [H, D] last), a row's channels contiguous")
+        n = len(lead)
+        return t.stride(n), t.stride(0) if n else 0
+
+    def _write(self, k, v, batch, layer, layers, stream):
+        ks, kl = self._kv("k", k, batch, layers)
+        vs, vl = self._kv("v", v, batch, layers)
+        capi.check(self._lib.cg_kv4_write(self._pool, self._ref, batch._ref, layer, 1 if layers is None else layers,
+                                          k.data_ptr(), v.data_ptr(), ks, vs, kl, vl, self._status, _stream(stream)),
+                   "cg_kv4_write")
+
+    def write(self, k: torch.Tensor, v: torch.Tensor, batch: Batch4, layer: int = 0, stream=None) -> None:
+        """Quantise the batch's rows of one layer into their slots. k, v:
+        [rows, H, D] or [rows, H*D], rows any stride apart."""
+        self._write(k, v, batch, layer, None, stream)
+
+    def write_layers(self, k: torch.Tensor, v: torch.Tensor, batch: Batch4, layer: int = 0, stream=None) -> None:
+        """write for the layers from `layer` on: k, v [layers, rows, H*D] (the
+        layout `codec.Codec.decompress_into` writes)."""
+        self._write(k, v, batch, layer, k.shape[0], stream)
+
+    def _read(self, batch, layer, layers, dtype, out, stream):
+        dtype = self.dtype if dtype is None else dtype
+        if dtype not in (self.dtype, torch.float32):
+            raise TypeError(f"a read gives {self.dtype} or torch.float32")
+        shape = (batch.rows, self.H, self.D) if layers is None else (layers, batch.rows, self.H * self.D)
+        if out is None:
+            k, v = (torch.empty(shape, dtype=dtype, device=self.pool.device) for _ in range(2))
+        else:
+            k, v = out
+            if k.dtype != dtype or v.dtype != dtype or k.device != self.pool.device or v.device != k.device:
+                raise TypeError(f"out must be two {dtype} tensors on the cache's device")
+            if tuple(k.shape) != shape or v.shape != k.shape or k.stride() != v.stride() or k.stride(-1) != 1 or \
+                    (layers is None and self.H > 1 and k.stride(1) != self.D):
+                raise ValueError(f"out must be two tensors {list(shape)} of equal strides, a row's channels contiguous")
+        n = 0 if layers is None else 1
+        capi.check(self._lib.cg_kv4_read(self._pool, self._ref, batch._ref, layer, 1 if layers is None else layers,
+                                         int(dtype == torch.float32), k.data_ptr(), v.data_ptr(), k.stride(n),
+                                         k.stride(0) if n else 0, self._status, _stream(stream)), "cg_kv4_read")
+        return k, v
+
+    def read(self, batch: Batch4, layer: int = 0, dtype: torch.dtype | None = None, out=None, stream=None):
+        """The batch's rows of one layer out of their slots -> (k, v) [rows, H,
+        D], in the cache's type or float32. A whole context is a batch whose
+        sequences have kv_len rows each."""
+        return self._read(batch, layer, None, dtype, out, stream)
+
+    def read_layers(self, batch: Batch4, layer: int = 0, layers: int | None = None, dtype: torch.dtype | None = None,
+                    out=None, stream=None):
+        """read for `layers` layers (default: the rest) -> (k, v) [layers, rows, H*D]."""
+        return self._read(batch, layer, self.L - layer if layers is None else layers, dtype, out, stream)
+
+    def attend(self, q: torch.Tensor, batch: Batch4, layer: int = 0, scale: float | None = None, window: int = 0,
+               return_lse: bool = False, out: torch.Tensor | None = None, stream=None):
+        """Causal attention of the batch's rows over their sequences, read where
+        they lie in the pool. q [rows, Hq, D], Hq a multiple of H; each row
+        sees the tokens up to its own position (with window > 0 the last
+        `window` of them), which have to be written before. scale defaults to
+        D**-0.5. -> out [rows, Hq, D], with return_lse also the natural
+        log-sum-exp of the scaled scores, float32 [rows, Hq] (-inf, and out 0,
+        where a row sees nothing)."""
+        if q.dtype != self.dtype:
+            raise TypeError(f"q must be {self.dtype}")
+        if q.device != self.pool.device:
+            raise ValueError("q must be on the cache's device")
+        D = self.D
+        if q.dim() != 3 or q.shape[0] != batch.rows or q.shape[2] != D or q.stride(2) != 1 or \
+                (q.shape[1] > 1 and q.stride(1) != D):
+            raise ValueError(f"q must be [{batch.rows}, Hq, {D}], a row's channels contiguous")
+        Hq = q.shape[1]
+        if Hq == 0 or Hq % self.H:
+            raise ValueError(f"the query heads ({Hq}) must be a multiple of the cache's {self.H}")
+        with torch.cuda.stream(stream):  # memory for the call belongs to its stream
+            if out is None:
+                out = torch.empty((batch.rows, Hq, D), dtype=q.dtype, device=q.device)
+            elif out.dtype != q.dtype or out.shape != q.shape or out.device != q.device or out.stride(2) != 1 or \
+                    (Hq > 1 and out.stride(1) != D):
+                raise ValueError("out must be like q")
+            lse = torch.empty((batch.rows, Hq), dtype=torch.float32, device=q.device) if return_lse else None
+            need = int(self._lib.cg_kv4_attention_workspace_bytes(self._ref, batch._ref, Hq))
+            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+        capi.check(self._lib.cg_kv4_attention(
+            self._pool, self._ref, batch._ref, layer, Hq, q.data_ptr(), q.stride(0),
+            D ** -0.5 if scale is None else scale, window, out.data_ptr(), out.stride(0),
+            None if lse is None else lse.data_ptr(), ws.data_ptr(), need, self._status, _stream(stream)),
+            "cg_kv4_attention")
+        return (out, lse) if return_lse else out

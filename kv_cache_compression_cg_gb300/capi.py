@@ -14,10 +14,11 @@ HEADER = os.path.join(os.path.dirname(HERE), "include", "cachegen.h")
 
 CG_OK, CG_ERR_INVALID_ARG, CG_ERR_WORKSPACE, CG_ERR_CUDA = 0, 1, 2, 3
 CG_FLAG_NONFINITE, CG_FLAG_CAPACITY, CG_FLAG_CORRUPT, CG_FLAG_BAD_SYMBOL = 0x1, 0x2, 0x4, 0x8
-CG_FLAG_TIMEOUT = 0x10
+CG_FLAG_TIMEOUT, CG_FLAG_BATCH = 0x10, 0x20
 CG_MAX_LAYERS, CG_MAX_CHUNK_TOKENS, CG_MAX_CHANNELS = 1024, 1024, 65536
 CG_NOALLOC_WORKSPACE_BYTES = 64 << 20
 CG_OUT_F32, CG_OUT_F16 = 0, 1
+CG_DT_F16, CG_DT_BF16 = 0, 1
 
 _ERRORS = {CG_ERR_INVALID_ARG: "invalid argument", CG_ERR_WORKSPACE: "workspace too small",
            CG_ERR_CUDA: "CUDA launch failed"}
@@ -28,14 +29,24 @@ class cg_shape(C.Structure):
                 ("chunk_tokens", C.c_int32), ("layer_stride", C.c_int64)]
 
 
+class cg_kv4_shape(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("L", "pages", "page_tokens", "H", "D", "group", "dtype")]
+
+
+class cg_kv4_batch(C.Structure):
+    _fields_ = [(n, C.c_int32) for n in ("B", "max_pages", "rows", "max_rows")] + \
+               [(n, C.c_void_p) for n in ("table", "kv_len", "start")]
+
+
 class CodecError(RuntimeError):
     def __init__(self, code: int, fn: str):
         super().__init__(f"{fn}: {_ERRORS.get(code, 'error')} (cg_status {code})")
         self.code = code
 
 
-_p, _u64, _i32 = C.c_void_p, C.c_uint64, C.c_int32
+_p, _u64, _i32, _i64 = C.c_void_p, C.c_uint64, C.c_int32, C.c_int64
 _SHAPE = C.POINTER(cg_shape)
+_KV4, _KV4B = C.POINTER(cg_kv4_shape), C.POINTER(cg_kv4_batch)
 SIGNATURES = {
     "cg_num_streams": (_u64, [_SHAPE]),
     "cg_cdf_elems": (_u64, [_SHAPE, _p, _p]),
@@ -68,6 +79,13 @@ SIGNATURES = {
     "cg_dequantize_delta": (_i32, [_p, _p, _SHAPE, _p, _p, C.c_int32, _p, _p, _p, _p]),
     "cg_compress_chunk_ex": (_i32, [_p, _p, _SHAPE, _p, _p, C.c_int, C.c_int32, _p, _p, _p, _u64, _p, _p, _p,
                                     _u64, _p, _p]),
+    "cg_kv4_pool_bytes": (_u64, [_KV4]),
+    "cg_kv4_record_bytes": (_u64, [_KV4]),
+    "cg_kv4_write": (_i32, [_p, _KV4, _KV4B, _i32, _i32, _p, _p, _i64, _i64, _i64, _i64, _p, _p]),
+    "cg_kv4_read": (_i32, [_p, _KV4, _KV4B, _i32, _i32, _i32, _p, _p, _i64, _i64, _p, _p]),
+    "cg_kv4_attention_workspace_bytes": (_u64, [_KV4, _KV4B, _i32]),
+    "cg_kv4_attention": (_i32, [_p, _KV4, _KV4B, _i32, _i32, _p, _i64, C.c_float, _i32, _p, _i64, _p, _p, _u64, _p,
+                                _p]),
     "cg_version": (C.c_char_p, []),
 }
 

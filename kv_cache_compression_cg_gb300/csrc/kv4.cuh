@@ -1,0 +1,140 @@
+// kv4.cuh - definitions shared by the kernels of the 4-bit paged cache; its
+// specification (Z, U, N) and the pool's byte layout are in include/cachegen.h.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "cg_internal.cuh"
+
+namespace cg {
+
+// Geometry of one call, passed by value to the kernels.
+struct Kv4 {
+    int L, pages, P, H, D, G, dtype;
+    int B, max_pages, rows, max_rows;
+    const int *table, *kv_len, *start;
+    long long record;        // bytes of a 16-token record
+    long long page_stride;   // bytes between pages of a layer (H * P / 16 records)
+    long long layer_stride;  // bytes between layers
+};
+
+constexpr int kBlk = 16;  // tokens a record
+
+// Byte offsets inside a record.
+template <int D, int G>
+struct Rec {
+    static constexpr int NG = D / G;
+    static constexpr int kV = 8 * D;             // V codes
+    static constexpr int kPK = 16 * D;           // K parameters
+    static constexpr int kPV = 16 * D + 64 * NG; // V parameters
+    static constexpr int kBytes = 16 * D + 128 * NG;
+};
+
+__device__ __forceinline__ void raise_flag(int32_t *status, int bit) {
+    if (status) atomicOr(status, bit);
+}
+
+// Rows of sequence b that the call works on: first row and count, 0 rows where
+// the batch's own bounds leave the sequence out.
+__device__ __forceinline__ void seq_rows(const Kv4 &p, int b, int &first, int &n, int32_t *status) {
+    if (!p.start) {
+        first = b;
+        n = 1;
+        return;
+    }
+    first = p.start[b];
+    n = p.start[b + 1] - first;
+    if (n < 0) n = 0;
+    if (n > p.max_rows || (n > 0 && (first < 0 || n > p.rows - first))) {
+        raise_flag(status, CG_FLAG_BATCH);
+        n = 0;
+    }
+}
+
+// Tokens of sequence b that the table can hold.
+__device__ __forceinline__ int seq_len(const Kv4 &p, int b, int32_t *status) {
+    const int len = p.kv_len[b];
+    const long long most = (long long)p.max_pages * p.P;
+    if (len < 0 || len > most) {
+        raise_flag(status, CG_FLAG_BATCH);
+        return len < 0 ? 0 : (int)most;
+    }
+    return len;
+}
+
+// The sequence that has row r, or -1: the last b with start[b] <= r, if r lies
+// before start[b + 1] (sequences without rows share their start with the next).
+__device__ __forceinline__ int row_seq(const Kv4 &p, int r) {
+    if (!p.start) return r;
+    int lo = 0, hi = p.B;  // start[lo] <= r < start[hi], taking start[B] as past every row
+    if (p.start[0] > r) return -1;
+    while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (p.start[mid] <= r) lo = mid;
+        else hi = mid;
+    }
+    return r < p.start[lo + 1] ? lo : -1;
+}
+
+// Position of row r of the batch in its sequence: false where the row is not
+// worked on at all; pos < 0 (or past the table) where it has no slot.
+__device__ __forceinline__ bool row_pos(const Kv4 &p, int r, int &b, long long &pos, int32_t *status) {
+    b = row_seq(p, r);
+    if (b < 0) return false;
+    int first, n;
+    seq_rows(p, b, first, n, status);
+    if (n == 0) return false;
+    pos = (long long)p.kv_len[b] - n + (r - first);
+    return true;
+}
+
+// The page of position pos of sequence b, -1 (flagged) where there is none.
+__device__ __forceinline__ int page_of(const Kv4 &p, int b, long long pos, int32_t *status) {
+    if (pos < 0) return -1;
+    if (pos >= (long long)p.max_pages * p.P) {
+        raise_flag(status, CG_FLAG_BATCH);
+        return -1;
+    }
+    const int page = p.table[(long long)b * p.max_pages + (int)(pos / p.P)];
+    if (page < 0 || page >= p.pages) {
+        raise_flag(status, CG_FLAG_BATCH);
+        return -1;
+    }
+    return page;
+}
+
+template <bool BF>
+__device__ __forceinline__ float bits_to_float(unsigned h) {
+    if (BF) return __uint_as_float(h << 16);
+    return __half2float(__ushort_as_half((unsigned short)h));
+}
+template <bool BF>
+__device__ __forceinline__ unsigned float_to_bits(float x) {
+    if (BF) return __bfloat16_as_ushort(__float2bfloat16_rn(x));
+    return __half_as_ushort(__float2half_rn(x));
+}
+
+// ---- launchers -------------------------------------------------------------
+cudaError_t launch_kv4_write(uint8_t *pool, const Kv4 &p, int layer, int nlayers, const void *k, const void *v,
+                             long long krs, long long vrs, long long kls, long long vls, int32_t *status,
+                             cudaStream_t s);
+cudaError_t launch_kv4_read(const uint8_t *pool, const Kv4 &p, int layer, int nlayers, bool f32, void *ok, void *ov,
+                            long long rs, long long ls, int32_t *status, cudaStream_t s);
+
+struct Kv4Attend {
+    const uint8_t *pool;  // of the layer
+    const uint16_t *q;
+    uint16_t *out;
+    float *lse;
+    long long q_stride, out_stride;
+    int Hq, R;     // query heads; of them for each KV head
+    float scale;
+    int window;    // 0: none
+    int32_t *status;
+    void *ws;
+};
+
+cudaError_t launch_kv4_step(const Kv4 &p, const Kv4Attend &a, cudaStream_t s);
+
+}  // namespace cg

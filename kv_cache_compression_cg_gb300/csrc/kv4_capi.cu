@@ -1,0 +1,151 @@
+// kv4_capi.cu - the C ABI of the 4-bit paged cache (include/cachegen.h):
+// argument checks on the host and launches on the caller's stream.
+#include "kv4.cuh"
+
+namespace {
+
+using cg::Kv4;
+
+bool shape_ok(const cg_kv4_shape *s) {
+    if (!s) return false;
+    if (s->L < 1 || s->L > CG_MAX_LAYERS || s->pages < 1 || s->H < 1 || s->H > 1024) return false;
+    if (s->page_tokens < 16 || s->page_tokens > 1024 || s->page_tokens % 16) return false;
+    if (s->D != 64 && s->D != 128 && s->D != 256) return false;
+    if ((s->group != 32 && s->group != 64 && s->group != 128) || s->group > s->D) return false;
+    return s->dtype == CG_DT_F16 || s->dtype == CG_DT_BF16;
+}
+
+uint64_t record_bytes(const cg_kv4_shape *s) { return 16ull * s->D + 128ull * (s->D / s->group); }
+
+uint64_t pool_bytes(const cg_kv4_shape *s) {
+    return record_bytes(s) * (uint64_t)(s->page_tokens / 16) * s->H * (uint64_t)s->pages * s->L;
+}
+
+bool batch_ok(const cg_kv4_batch *b) {
+    if (!b || b->B < 0 || b->rows < 0 || b->max_rows < 0 || b->max_pages < 0) return false;
+    if (!b->start && (b->rows != b->B || (b->B > 0 && b->max_rows < 1))) return false;
+    return true;
+}
+
+bool aligned(const void *p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+bool arrays_ok(const cg_kv4_batch *b) {
+    return b->table && b->kv_len && aligned(b->table, 4) && aligned(b->kv_len, 4) && aligned(b->start, 4);
+}
+
+void prepare(const cg_kv4_shape *s, const cg_kv4_batch *b, Kv4 &p) {
+    p.L = s->L;
+    p.pages = s->pages;
+    p.P = s->page_tokens;
+    p.H = s->H;
+    p.D = s->D;
+    p.G = s->group;
+    p.dtype = s->dtype;
+    p.B = b->B;
+    p.max_pages = b->max_pages;
+    p.rows = b->rows;
+    p.max_rows = b->max_rows;
+    p.table = b->table;
+    p.kv_len = b->kv_len;
+    p.start = b->start;
+    p.record = (long long)record_bytes(s);
+    p.page_stride = p.record * (p.P / 16) * p.H;
+    p.layer_stride = p.page_stride * p.pages;
+}
+
+bool layers_ok(const cg_kv4_shape *s, int32_t layer, int32_t n) {
+    return layer >= 0 && n >= 0 && layer <= s->L && n <= s->L - layer;
+}
+
+bool strides_ok(const cg_kv4_shape *s, const cg_kv4_batch *b, int32_t n, int64_t row, int64_t layer) {
+    const int64_t C = (int64_t)s->H * s->D;
+    if (b->rows > 1 && row < C) return false;
+    if (n > 1 && (layer < 0 || (row >= 0 && b->rows > 0 && layer < (b->rows - 1) * row + C))) return false;
+    return row >= 0;
+}
+
+cg_status launched(cudaError_t e) { return e == cudaSuccess ? CG_OK : CG_ERR_CUDA; }
+
+}  // namespace
+
+extern "C" {
+
+uint64_t cg_kv4_pool_bytes(const cg_kv4_shape *shape) { return shape_ok(shape) ? pool_bytes(shape) : 0; }
+
+uint64_t cg_kv4_record_bytes(const cg_kv4_shape *shape) { return shape_ok(shape) ? record_bytes(shape) : 0; }
+
+cg_status cg_kv4_write(uint8_t *pool, const cg_kv4_shape *shape, const cg_kv4_batch *batch, int32_t layer,
+                       int32_t nlayers, const void *k, const void *v, int64_t k_row_stride, int64_t v_row_stride,
+                       int64_t k_layer_stride, int64_t v_layer_stride, int32_t *status, cudaStream_t stream) {
+    CG_TRACE_RANGE();
+    if (!shape_ok(shape) || !batch_ok(batch) || !layers_ok(shape, layer, nlayers)) return CG_ERR_INVALID_ARG;
+    if (!strides_ok(shape, batch, nlayers, k_row_stride, k_layer_stride) ||
+        !strides_ok(shape, batch, nlayers, v_row_stride, v_layer_stride))
+        return CG_ERR_INVALID_ARG;
+    if (batch->rows == 0 || batch->B == 0 || nlayers == 0) return CG_OK;
+    if (!pool || !k || !v || !arrays_ok(batch) || !aligned(pool, 16) || !aligned(k, 2) || !aligned(v, 2) ||
+        !aligned(status, 4))
+        return CG_ERR_INVALID_ARG;
+    Kv4 p;
+    prepare(shape, batch, p);
+    return launched(cg::launch_kv4_write(pool, p, layer, nlayers, k, v, k_row_stride, v_row_stride, k_layer_stride,
+                                         v_layer_stride, status, stream));
+}
+
+cg_status cg_kv4_read(const uint8_t *pool, const cg_kv4_shape *shape, const cg_kv4_batch *batch, int32_t layer,
+                      int32_t nlayers, int32_t out_f32, void *out_k, void *out_v, int64_t row_stride,
+                      int64_t layer_stride, int32_t *status, cudaStream_t stream) {
+    CG_TRACE_RANGE();
+    if (!shape_ok(shape) || !batch_ok(batch) || !layers_ok(shape, layer, nlayers) ||
+        !strides_ok(shape, batch, nlayers, row_stride, layer_stride))
+        return CG_ERR_INVALID_ARG;
+    if (batch->rows == 0 || batch->B == 0 || nlayers == 0) return CG_OK;
+    const uintptr_t es = out_f32 ? 4 : 2;
+    if (!pool || !out_k || !out_v || !arrays_ok(batch) || !aligned(pool, 16) || !aligned(out_k, es) ||
+        !aligned(out_v, es) || !aligned(status, 4))
+        return CG_ERR_INVALID_ARG;
+    Kv4 p;
+    prepare(shape, batch, p);
+    return launched(cg::launch_kv4_read(pool, p, layer, nlayers, out_f32 != 0, out_k, out_v, row_stride,
+                                        layer_stride, status, stream));
+}
+
+uint64_t cg_kv4_attention_workspace_bytes(const cg_kv4_shape *shape, const cg_kv4_batch *batch, int32_t Hq) {
+    if (!shape_ok(shape) || !batch_ok(batch) || Hq < 1 || Hq % shape->H) return 0;
+    return 256;
+}
+
+cg_status cg_kv4_attention(const uint8_t *pool, const cg_kv4_shape *shape, const cg_kv4_batch *batch, int32_t layer,
+                           int32_t Hq, const void *q, int64_t q_row_stride, float scale, int32_t window, void *out,
+                           int64_t out_row_stride, float *lse, void *workspace, uint64_t workspace_bytes,
+                           int32_t *status, cudaStream_t stream) {
+    CG_TRACE_RANGE();
+    if (!shape_ok(shape) || !batch_ok(batch) || !layers_ok(shape, layer, 1)) return CG_ERR_INVALID_ARG;
+    if (Hq < 1 || Hq % shape->H || Hq > 65536) return CG_ERR_INVALID_ARG;
+    const int64_t row = (int64_t)Hq * shape->D;
+    if (q_row_stride < 0 || out_row_stride < 0 || (batch->rows > 1 && (q_row_stride < row || out_row_stride < row)))
+        return CG_ERR_INVALID_ARG;
+    if (batch->rows == 0 || batch->B == 0) return CG_OK;
+    if (!pool || !q || !out || !workspace || !arrays_ok(batch) || !aligned(pool, 16) || !aligned(q, 2) ||
+        !aligned(out, 2) || !aligned(lse, 4) || !aligned(workspace, 256) || !aligned(status, 4))
+        return CG_ERR_INVALID_ARG;
+    if (workspace_bytes < cg_kv4_attention_workspace_bytes(shape, batch, Hq)) return CG_ERR_WORKSPACE;
+    Kv4 p;
+    prepare(shape, batch, p);
+    cg::Kv4Attend a;
+    a.pool = pool + (long long)layer * p.layer_stride;
+    a.q = static_cast<const uint16_t *>(q);
+    a.out = static_cast<uint16_t *>(out);
+    a.lse = lse;
+    a.q_stride = q_row_stride;
+    a.out_stride = out_row_stride;
+    a.Hq = Hq;
+    a.R = Hq / shape->H;
+    a.scale = scale;
+    a.window = window > 0 ? window : 0;
+    a.status = status;
+    a.ws = workspace;
+    return launched(cg::launch_kv4_step(p, a, stream));
+}
+
+}  // extern "C"

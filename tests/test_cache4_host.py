@@ -1,0 +1,151 @@
+"""Host-side checks of the 4-bit paged cache (no GPU): sizes, refusals before
+any device work, and the reference's own layout."""
+import ctypes as C
+
+import numpy as np
+import pytest
+
+from cache4_reference import Layout, from16, quantise, to16, values
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from kv_cache_compression_cg_gb300 import build, capi
+    build.build()
+    return capi.load()
+
+
+FAKE, ODD, WS = 0x1000, 0x1001, 0x10000  # never dereferenced
+
+
+def shape(**kw):
+    from kv_cache_compression_cg_gb300 import capi
+    d = dict(L=2, pages=10, page_tokens=32, H=4, D=128, group=64, dtype=0)
+    d.update(kw)
+    return capi.cg_kv4_shape(**d)
+
+
+def batch(**kw):
+    from kv_cache_compression_cg_gb300 import capi
+    d = dict(B=3, max_pages=4, rows=3, max_rows=1, table=FAKE, kv_len=FAKE, start=None)
+    d.update(kw)
+    return capi.cg_kv4_batch(**d)
+
+
+BAD_SHAPES = [dict(L=0), dict(L=1025), dict(pages=0), dict(page_tokens=8), dict(page_tokens=24), dict(page_tokens=1040),
+              dict(H=0), dict(H=1025), dict(D=96), dict(D=0), dict(group=16), dict(group=256), dict(D=64, group=128), dict(dtype=2)]
+BAD_BATCHES = [dict(B=-1), dict(rows=-1), dict(rows=4), dict(max_rows=0), dict(max_pages=-1), dict(table=None),
+               dict(kv_len=None), dict(table=0x1002), dict(kv_len=ODD), dict(start=ODD)]
+
+
+def write(lib, s, b, layer=0, n=1, pool=FAKE, k=FAKE, v=FAKE, krs=512, vrs=512, kls=0, vls=0, status=None):
+    return lib.cg_kv4_write(pool, C.byref(s), C.byref(b), layer, n, k, v, krs, vrs, kls, vls, status, None)
+
+
+def read(lib, s, b, layer=0, n=1, f32=0, pool=FAKE, k=FAKE, v=FAKE, rs=512, ls=0):
+    return lib.cg_kv4_read(pool, C.byref(s), C.byref(b), layer, n, f32, k, v, rs, ls, None, None)
+
+
+def attend(lib, s, b, layer=0, Hq=8, pool=FAKE, q=FAKE, qs=1024, window=0, out=FAKE, os=1024, lse=None, ws=WS, wsb=1 << 40):
+    return lib.cg_kv4_attention(pool, C.byref(s), C.byref(b), layer, Hq, q, qs, 0.1, window, out, os, lse, ws, wsb, None, None)
+
+
+def test_sizes(lib):
+    for L, pages, P, H, D, G in [(1, 1, 16, 1, 64, 64), (2, 10, 32, 4, 128, 64), (3, 7, 128, 5, 256, 32), (32, 1000, 64, 8, 128, 128)]:
+        s = shape(L=L, pages=pages, page_tokens=P, H=H, D=D, group=G)
+        lay = Layout(L, pages, P, H, D, G)
+        assert lib.cg_kv4_pool_bytes(C.byref(s)) == lay.nbytes
+        assert lib.cg_kv4_record_bytes(C.byref(s)) == lay.record
+
+
+@pytest.mark.parametrize("bad", BAD_SHAPES)
+def test_shapes_refused(lib, bad):
+    s, b = shape(**bad), batch()
+    assert lib.cg_kv4_pool_bytes(C.byref(s)) == 0
+    assert lib.cg_kv4_record_bytes(C.byref(s)) == 0
+    assert lib.cg_kv4_attention_workspace_bytes(C.byref(s), C.byref(b), 8) == 0
+    assert write(lib, s, b) == 1 and read(lib, s, b) == 1 and attend(lib, s, b) == 1
+
+
+@pytest.mark.parametrize("bad", BAD_BATCHES)
+def test_batches_refused(lib, bad):
+    s, b = shape(), batch(**bad)
+    assert write(lib, s, b) == 1 and read(lib, s, b) == 1 and attend(lib, s, b) == 1
+
+
+def test_arguments_refused(lib):
+    s, b = shape(), batch()
+    for kw in (dict(pool=None), dict(pool=0x1008), dict(k=None), dict(v=ODD), dict(layer=-1), dict(layer=2), dict(n=3),
+               dict(n=-1), dict(krs=511), dict(vrs=-512), dict(n=2, kls=100, vls=4096), dict(n=2, kls=4096, vls=-1), dict(status=ODD)):
+        assert write(lib, s, b, **kw) == 1, kw
+    for kw in (dict(pool=None), dict(k=None), dict(v=ODD), dict(layer=2), dict(n=3), dict(rs=511), dict(n=2, ls=100),
+               dict(f32=1, k=0x1002)):
+        assert read(lib, s, b, **kw) == 1, kw
+    for kw in (dict(pool=None), dict(pool=0x1008), dict(q=None), dict(q=ODD), dict(out=None), dict(ws=None), dict(ws=0x1010),
+               dict(Hq=0), dict(Hq=6), dict(Hq=-4), dict(layer=2), dict(layer=-1), dict(qs=1023), dict(os=1023), dict(lse=0x1002)):
+        assert attend(lib, s, b, **kw) == 1, kw
+    need = lib.cg_kv4_attention_workspace_bytes(C.byref(s), C.byref(b), 8)
+    assert need > 0 and need % 256 == 0
+    assert attend(lib, s, b, wsb=need - 1) == 2
+    assert lib.cg_kv4_attention_workspace_bytes(C.byref(s), C.byref(b), 6) == 0
+
+
+def test_nothing_to_do_is_no_error(lib):
+    s = shape()
+    for b in (batch(B=0, rows=0, table=None, kv_len=None), batch(rows=0, max_rows=0, start=FAKE)):
+        assert write(lib, s, b) == 0 and read(lib, s, b) == 0 and attend(lib, s, b) == 0
+    assert write(lib, s, batch(), n=0) == 0
+
+
+def test_wrappers_refuse(lib):
+    import torch
+    from kv_cache_compression_cg_gb300 import cache4
+    i = torch.zeros(2, 3, dtype=torch.int32)
+    with pytest.raises(TypeError):
+        cache4.Batch4(i.long(), i[:, 0])
+    with pytest.raises(ValueError, match="CUDA"):
+        cache4.Batch4(i, torch.zeros(2, dtype=torch.int32))
+    with pytest.raises(TypeError):
+        cache4.Cache4(1, 1, 16, 1, 64, dtype=torch.float32)
+    with pytest.raises(ValueError, match="invalid shape"):
+        cache4.Cache4(1, 1, 16, 1, 80)
+    with pytest.raises(ValueError, match="pool"):
+        cache4.Cache4(1, 1, 16, 1, 64, pool=torch.zeros(1152, dtype=torch.uint8))
+
+
+def test_reference_layout_is_a_bijection():
+    """Every byte of a record belongs to exactly one token, channel or parameter."""
+    for D, G in ((64, 32), (128, 64), (256, 128), (256, 32)):
+        lay = Layout(1, 1, 16, 1, D, G)
+        nibbles, params = set(), set()
+        for slot in range(16):
+            for v in (False, True):
+                at, sh = (lay.v_nibbles if v else lay.k_nibbles)(slot)
+                nibbles |= {2 * int(a) + int(s) // 4 for a, s in zip(at, sh)}
+                params |= set(range(lay.params(slot, v), lay.params(slot, v) + 4 * lay.ng))
+        assert nibbles == set(range(2 * 16 * D))
+        assert params == set(range(16 * D, lay.record))
+
+
+@pytest.mark.parametrize("bf16", [False, True])
+def test_reference_quantiser(bf16):
+    """Its error is at most half a step and what the scale's rounding clips; a
+    scale times a code has at most 11 significant bits; ties go to even."""
+    rng = np.random.default_rng(1)
+    x = from16(to16((rng.standard_normal((50, 256)) * np.exp(rng.standard_normal((50, 1)))).astype(np.float32), bf16), bf16)
+    for group in (32, 64, 128):
+        c, p = quantise(x, group, bf16)
+        y = values(c, p, group, bf16)
+        s = np.repeat(from16(p[..., 0], bf16), group, -1)
+        assert (np.abs(x - y) <= s * (0.5 + 15 * 2.0 ** -7) + np.abs(x) * 2.0 ** -22).all()
+        prod = (c * s).astype(np.float64)
+        m, e = np.frexp(prod)
+        assert (np.abs(m) * 2 ** 11 == np.rint(np.abs(m) * 2 ** 11)).all()
+    tie = np.zeros((1, 32), np.float32)
+    tie[0, :4] = [15.0, 0.5, 1.5, 2.5]
+    c, p = quantise(tie, 32, bf16)
+    assert c[0, :4].tolist() == [15, 0, 2, 2] and from16(p[0, 0], bf16).tolist() == [1.0, 0.0]
+    bad = np.ones((1, 64), np.float32)
+    bad[0, 3] = np.inf
+    c, p = quantise(bad, 32, bf16)
+    assert np.isnan(from16(p[0, 0], bf16)).all() and (c == 0).all() and from16(p[0, 1], bf16).tolist() == [0.0, 1.0]
