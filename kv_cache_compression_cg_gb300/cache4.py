@@ -104,6 +104,17 @@ class Cache4:
         self.pool = pool
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self._pool, self._status = pool.data_ptr(), self.status.data_ptr()
+        self._ws: dict[int, torch.Tensor] = {}  # attention's workspace of each stream
+
+    def _workspace(self, stream: int, need: int) -> torch.Tensor:
+        """The stream's workspace. Calls on one stream follow one another and may
+        share it; a captured call, which may be replayed on any, gets its own."""
+        ws = self._ws.get(stream)
+        if ws is None or ws.numel() < need or torch.cuda.is_current_stream_capturing():
+            ws = torch.zeros(need, dtype=torch.uint8, device=self.pool.device)
+            if not torch.cuda.is_current_stream_capturing():
+                self._ws[stream] = ws
+        return ws
 
     def _kv(self, name, t, batch, layers):
         """Strides (row, layer) of t: [rows, H, D] or [rows, H*D], with a dimension of layers before where there are several."""
@@ -200,7 +211,7 @@ class Cache4:
                 raise ValueError("out must be like q")
             lse = torch.empty((batch.rows, Hq), dtype=torch.float32, device=q.device) if return_lse else None
             need = int(self._lib.cg_kv4_attention_workspace_bytes(self._ref, batch._ref, Hq))
-            ws = torch.empty(need, dtype=torch.uint8, device=q.device)
+            ws = self._workspace(_stream(stream), need)
         capi.check(self._lib.cg_kv4_attention(
             self._pool, self._ref, batch._ref, layer, Hq, q.data_ptr(), q.stride(0),
             D ** -0.5 if scale is None else scale, window, out.data_ptr(), out.stride(0),

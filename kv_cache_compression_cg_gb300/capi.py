@@ -84,6 +84,7 @@ SIGNATURES = {
     "cg_kv4_write": (_i32, [_p, _KV4, _KV4B, _i32, _i32, _p, _p, _i64, _i64, _i64, _i64, _p, _p]),
     "cg_kv4_read": (_i32, [_p, _KV4, _KV4B, _i32, _i32, _i32, _p, _p, _i64, _i64, _p, _p]),
     "cg_kv4_attention_workspace_bytes": (_u64, [_KV4, _KV4B, _i32]),
+    "cg_kv4_ticket_bytes": (_u64, []),
     "cg_kv4_attention": (_i32, [_p, _KV4, _KV4B, _i32, _i32, _p, _i64, C.c_float, _i32, _p, _i64, _p, _p, _u64, _p,
                                 _p]),
     "cg_version": (C.c_char_p, []),

@@ -132,8 +132,13 @@ struct Kv4Attend {
     float scale;
     int window;    // 0: none
     int32_t *status;
-    void *ws;
+    void *ws;                 // tickets (ticket_bytes, zero between calls), then partial results
+    long long ticket_bytes;
+    bool q_vec, out_vec;      // rows allow 8-byte loads, stores
 };
+
+uint64_t kv4_ticket_bytes();
+uint64_t kv4_step_workspace_bytes(const Kv4 &p);
 
 cudaError_t launch_kv4_step(const Kv4 &p, const Kv4Attend &a, cudaStream_t s);
 

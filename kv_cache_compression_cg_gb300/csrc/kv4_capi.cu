@@ -72,6 +72,8 @@ extern "C" {
 
 uint64_t cg_kv4_pool_bytes(const cg_kv4_shape *shape) { return shape_ok(shape) ? pool_bytes(shape) : 0; }
 
+uint64_t cg_kv4_ticket_bytes(void) { return cg::kv4_ticket_bytes(); }
+
 uint64_t cg_kv4_record_bytes(const cg_kv4_shape *shape) { return shape_ok(shape) ? record_bytes(shape) : 0; }
 
 cg_status cg_kv4_write(uint8_t *pool, const cg_kv4_shape *shape, const cg_kv4_batch *batch, int32_t layer,
@@ -112,7 +114,9 @@ cg_status cg_kv4_read(const uint8_t *pool, const cg_kv4_shape *shape, const cg_k
 
 uint64_t cg_kv4_attention_workspace_bytes(const cg_kv4_shape *shape, const cg_kv4_batch *batch, int32_t Hq) {
     if (!shape_ok(shape) || !batch_ok(batch) || Hq < 1 || Hq % shape->H) return 0;
-    return 256;
+    Kv4 p;
+    prepare(shape, batch, p);
+    return (cg::kv4_step_workspace_bytes(p) + 255) / 256 * 256;
 }
 
 cg_status cg_kv4_attention(const uint8_t *pool, const cg_kv4_shape *shape, const cg_kv4_batch *batch, int32_t layer,
@@ -145,6 +149,9 @@ cg_status cg_kv4_attention(const uint8_t *pool, const cg_kv4_shape *shape, const
     a.window = window > 0 ? window : 0;
     a.status = status;
     a.ws = workspace;
+    a.ticket_bytes = (long long)cg::kv4_ticket_bytes();
+    a.q_vec = aligned(q, 8) && q_row_stride % 4 == 0;
+    a.out_vec = aligned(out, 8) && out_row_stride % 4 == 0;
     return launched(cg::launch_kv4_step(p, a, stream));
 }
 

@@ -1,91 +1,733 @@
-// kv4_step.cu - attention over the 4-bit paged cache (N in include/cachegen.h).
+// kv4_step.cu - attention of few query rows over the 4-bit paged cache (N in
+// include/cachegen.h): a token's step, drafted tokens.
 //
-// One CTA a (row, query head); its warps take every fourth key, the lanes the
-// channels; an online softmax a warp, joined through shared memory at the end.
+// The columns of one work item are (row, query head) pairs that share a KV
+// head; every key is read once for all of them. The products run on
+// mma.m16n8k16 with the codes as the left operand: a nibble in its place in a 16-bit half is the
+// subnormal binary16 number c * 2^-24 (or c * 2^-20), so one AND makes two operands of
+// eight codes' word and nothing has to be subtracted.
+//   scores   S = sum over groups of s_g (c . q)_g + m_g (sum of q over the group): the codes' products are
+//            exact, s and m enter in binary32 after the group's matrix instructions;
+//   values   V^ = c s + m, one rounding to binary16, under a power of two (sigma) that
+//            follows the largest |V^| seen; weights in binary16, sums in binary32.
+// A warp keeps a softmax of its own (running maximum, sum, accumulators);
+// warps of a CTA take 32-token tiles in turn and join in shared memory.
+//
+// The work of a call (all items' units of 128 tokens, known on the device only) is dealt out in
+// equal contiguous ranges to a grid that fills the GPU; an item that several CTAs share
+// is joined by the last of them to finish, in the order of the ranges, so the
+// result does not depend on which that is.
 #include "kv4.cuh"
 
 namespace cg {
 namespace {
 
+constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kTile = 32;              // tokens a warp takes at a time: two records
+constexpr int kUnit = kTile * kWarps;  // tokens the work is dealt out in
+constexpr int kSigMin = -110;            // values below 2^-115 or so lose bits
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+
+template <int D>
+__host__ __device__ constexpr int stages() { return D == 256 ? 2 : 3; }
+template <int D, int G>
+__host__ __device__ constexpr int ring_bytes() { return kWarps * stages<D>() * 2 * Rec<D, G>::kBytes; }
+
+__device__ __forceinline__ void mma(float *c, unsigned a0, unsigned a1, unsigned a2, unsigned a3, unsigned b0,
+                                    unsigned b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ unsigned transposed(unsigned x) {
+    unsigned y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
+}
+__device__ __forceinline__ unsigned pack_half(float lo, float hi) {
+    unsigned y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+__device__ __forceinline__ unsigned fma_half(unsigned a, unsigned b, unsigned c) {
+    unsigned y;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+    return y;
+}
+__device__ __forceinline__ float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ void copy16(unsigned smem, const uint8_t *g) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void copy_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ float pow2f(int e) {  // 2^e, e in [-126, 127]
+    return __int_as_float((e + 127) << 23);
+}
+
+// What a sequence asks of the call.
+struct Seq {
+    int first, n;      // rows
+    int len;           // tokens
+    int u0, units;     // first unit of 128 tokens that some row sees, and how many
+    int tiles;         // column tiles
+};
+__device__ __forceinline__ Seq seq_of(const Kv4 &p, const Kv4Attend &a, int b, int cols, int32_t *status) {
+    Seq s;
+    seq_rows(p, b, s.first, s.n, status);
+    s.len = s.n ? seq_len(p, b, status) : 0;
+    s.u0 = 0;
+    s.units = 0;
+    s.tiles = 0;
+    if (s.n) {
+        const long long pos0 = (long long)p.kv_len[b] - s.n;  // of the first row; may be negative
+        const long long lo = a.window && pos0 + 1 > a.window ? pos0 + 1 - a.window : 0;
+        s.u0 = (int)((lo < s.len ? lo : s.len) / kUnit);
+        const int u1 = (s.len + kUnit - 1) / kUnit;
+        s.units = u1 > s.u0 ? u1 - s.u0 : 1;  // a sequence without keys still has outputs
+        s.tiles = (s.n * a.R + cols - 1) / cols;
+    }
+    return s;
+}
+
+// Partial result of a CTA for one item: [cols][D] accumulators in units of sigma = 1, then per column
+// maximum, sum and the bits of groups that are not finite.
+template <int D, int COLS>
+struct Partial {
+    static constexpr int kFloats = COLS * D + 3 * COLS;
+};
+
+// Four channels d.. of one column's result: sums x under maximum top, weights' sum tl, bits of groups that are not finite.
 template <int D, int G, bool BF>
-__global__ void __launch_bounds__(128) k_kv4_rows(Kv4 p, Kv4Attend a) {
+__device__ __forceinline__ void put_out(const Kv4Attend &a, const Seq &s, int kvh, int col, int d, float4 x, float top,
+                                        float tl, unsigned bits) {
+    const int row = s.first + col / a.R, h = kvh * a.R + col % a.R;
+    const float inv = tl == 0.0f ? 0.0f : 1.0f / tl;
+    if ((bits >> (d / G)) & 1u) x.x = x.y = x.z = x.w = __uint_as_float(0x7FC00000u);
+    const unsigned w0 = float_to_bits<BF>(x.x * inv) | (float_to_bits<BF>(x.y * inv) << 16);
+    const unsigned w1 = float_to_bits<BF>(x.z * inv) | (float_to_bits<BF>(x.w * inv) << 16);
+    uint16_t *dst = a.out + (long long)row * a.out_stride + (long long)h * D + d;
+    if (a.out_vec) {
+        *reinterpret_cast<uint2 *>(dst) = make_uint2(w0, w1);
+    } else {
+        dst[0] = (uint16_t)w0, dst[1] = (uint16_t)(w0 >> 16), dst[2] = (uint16_t)w1, dst[3] = (uint16_t)(w1 >> 16);
+    }
+    if (a.lse && d == 0)
+        a.lse[(long long)row * a.Hq + h] = tl == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top) * kLn2 + logf(tl);
+}
+
+// The CTA whose range [total * c / grid, total * (c + 1) / grid) has unit u.
+__device__ __forceinline__ long long cta_of(long long u, long long total, long long grid) {
+    long long c = u * grid / total;
+    while (total * c / grid > u) c--;
+    while (total * (c + 1) / grid <= u) c++;
+    return c;
+}
+
+template <int D, int G, int NT, bool BF>
+__global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
     using R = Rec<D, G>;
-    constexpr int N = D / 32;  // channels a lane: lane + 32 i
-    __shared__ float sm[4], sl[4], so[4][D];
-    const int row = blockIdx.x / a.Hq, h = blockIdx.x % a.Hq, kvh = h / a.R;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int b;
-    long long pos;
-    if (!row_pos(p, row, b, pos, a.status)) return;
-    const int len = seq_len(p, b, a.status);
-    const long long last = pos < len ? pos : (long long)len - 1;
-    const long long first = a.window && pos - a.window + 1 > 0 ? pos - a.window + 1 : 0;
-    float q[N], o[N], m = -INFINITY, l = 0.0f;
-#pragma unroll
-    for (int i = 0; i < N; i++) {
-        q[i] = bits_to_float<BF>(a.q[row * a.q_stride + (long long)h * D + lane + 32 * i]) * a.scale;
-        o[i] = 0.0f;
-    }
-    for (long long j = first + warp; j <= last; j += 4) {
-        const int page = page_of(p, b, j, a.status);
-        if (page < 0) continue;
-        const int at = (int)(j % p.P), tok = at % kBlk;
-        const uint8_t *rec = a.pool + page * p.page_stride + ((long long)kvh * (p.P / kBlk) + at / kBlk) * p.record;
-        float s = 0.0f, vv[N];
-#pragma unroll
-        for (int i = 0; i < N; i++) {
-            const int d = lane + 32 * i, w = d / 32, e = d % 16;
-            const int nib = 4 * (e & 1) + 2 * (d / 16 % 2) + ((e >> 1) & 1);
-            const unsigned kb = rec[tok * (D / 2) + (e / 4) * (D / 8) + w * 4 + nib / 2];
-            const unsigned kp = *reinterpret_cast<const unsigned *>(rec + R::kPK + (tok * R::NG + d / G) * 4);
-            s += q[i] * fmaf((float)((kb >> (4 * (nib & 1))) & 15u), bits_to_float<BF>(kp & 0xFFFFu),
-                             bits_to_float<BF>(kp >> 16));
-            const int g = d / (D / 8), c = d % (D / 8);
-            const unsigned vb = rec[R::kV + (tok >> 3) * (4 * D) + g * (D / 2) + (tok & 7) * (D / 16) + c / 2];
-            const unsigned vp = *reinterpret_cast<const unsigned *>(rec + R::kPV + (tok * R::NG + d / G) * 4);
-            vv[i] = fmaf((float)((vb >> (4 * (c & 1))) & 15u), bits_to_float<BF>(vp & 0xFFFFu),
-                         bits_to_float<BF>(vp >> 16));
-        }
-#pragma unroll
-        for (int x = 16; x; x >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, x);
-        const float top = fmaxf(m, s), f = expf(m - top), e = expf(s - top);
-        m = top;
-        l = l * f + e;
-#pragma unroll
-        for (int i = 0; i < N; i++) o[i] = o[i] * f + e * vv[i];
-    }
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
+    constexpr int NG = R::NG, COLS = 8 * NT, ST = stages<D>(), KS = D / 16, W = D / 32;
+    constexpr int RB = R::kBytes, TB = 2 * RB;
+    extern __shared__ __align__(16) uint8_t smem[];
+    __shared__ long long s_base[kWarps];
+    __shared__ long long s_mine;
+    __shared__ int s_b;
+    __shared__ int s_last;
+    __shared__ float s_m[kWarps][COLS], s_l[kWarps][COLS], s_sigma[kWarps];
+    __shared__ unsigned s_bits[kWarps][COLS];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
+
+    // ---- the total of all sequences' units, then the sequence that this CTA's range starts in
+    long long sum = 0;
+    for (int b = threadIdx.x; b < p.B; b += kThreads) {
+        const Seq s = seq_of(p, a, b, COLS, a.status);
+        sum += (long long)s.units * s.tiles * p.H;
     }
 #pragma unroll
-    for (int i = 0; i < N; i++) so[warp][lane + 32 * i] = o[i];
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) s_base[warp] = sum;
     __syncthreads();
-    float top = sm[0], total = 0.0f;
-    for (int w = 1; w < 4; w++) top = fmaxf(top, sm[w]);
-    float f[4];
-    for (int w = 0; w < 4; w++) {
-        f[w] = sm[w] == -INFINITY ? 0.0f : expf(sm[w] - top);
-        total += sl[w] * f[w];
+    const long long total = s_base[0] + s_base[1] + s_base[2] + s_base[3];
+    const long long grid = total < gridDim.x ? total : gridDim.x;
+    if (blockIdx.x >= grid) return;
+    long long u = total * blockIdx.x / grid;
+    const long long u_end = total * (blockIdx.x + 1) / grid;
+    int b = 0;
+    long long before = 0;  // units of the sequences before b
+    if (warp == 0) {
+        long long base = 0;
+        int at = 0;
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            long long x = 0;
+            if (b0 + lane < p.B) {
+                const Seq s = seq_of(p, a, b0 + lane, COLS, nullptr);
+                x = (long long)s.units * s.tiles * p.H;
+            }
+            long long incl = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, base + incl > u);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                at = b0 + src;
+                base += __shfl_sync(0xFFFFFFFFu, incl - x, src);
+                break;
+            }
+            base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
+        if (lane == 0) {
+            s_b = at;
+            s_mine = base;
+        }
     }
-    for (int d = threadIdx.x; d < D; d += 128) {
-        float x = 0.0f;
-        for (int w = 0; w < 4; w++) x += so[w][d] * f[w];
-        a.out[row * a.out_stride + (long long)h * D + d] =
-            (uint16_t)float_to_bits<BF>(top == -INFINITY ? 0.0f : x / total);
+    __syncthreads();
+    b = s_b;
+    before = s_mine;
+
+    unsigned *tickets = static_cast<unsigned *>(a.ws);
+    float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + a.ticket_bytes);
+    constexpr int PF = Partial<D, COLS>::kFloats;
+
+    uint8_t *ring = smem + warp * ST * TB;
+    const unsigned ring_s = (unsigned)__cvta_generic_to_shared(ring);
+
+    while (u < u_end) {
+        // ---- the item that unit u belongs to
+        Seq s = seq_of(p, a, b, COLS, nullptr);
+        long long all = (long long)s.units * s.tiles * p.H;
+        while (u - before >= all) {
+            before += all;
+            b++;
+            s = seq_of(p, a, b, COLS, nullptr);
+            all = (long long)s.units * s.tiles * p.H;
+        }
+        const int item = (int)((u - before) / s.units), ua = (int)((u - before) % s.units);
+        const long long left = u_end - u;
+        const int ub = left < s.units - ua ? ua + (int)left : s.units;
+        const int kvh = item % p.H, ct = item / p.H;
+        const long long item_u0 = u - ua, item_u1 = item_u0 + s.units;
+        const long long pos0 = (long long)p.kv_len[b] - s.n;
+
+        // ---- copies of the first tiles
+        const int its = ub - ua;
+        const int tok0 = (s.u0 + ua) * kUnit + warp * kTile;  // this warp's first tile; the next ones kUnit apart
+        const int *table = p.table + (long long)b * p.max_pages;
+        const int rpp = p.P / kBlk;
+        int pg = -1;  // lane i: page of record i (two a tile) of the 16 tiles from tile pg_at on
+        auto pages_from = [&](int it) {
+            const long long tok = tok0 + (long long)(it + (lane >> 1)) * kUnit + (lane & 1) * kBlk;
+            pg = -1;
+            if (it + (lane >> 1) < its && tok < s.len) {
+                pg = table[(int)(tok / p.P)];
+                if (pg < 0 || pg >= p.pages) {
+                    raise_flag(a.status, CG_FLAG_BATCH);
+                    pg = -1;
+                }
+            }
+        };
+        unsigned ok_now = 0;  // two bits a tile in the ring, by stage: records that have a page
+        auto issue = [&](int it) {
+            if ((it & 15) == 0) pages_from(it);
+            const int st = it % ST;
+            const int p0 = __shfl_sync(0xFFFFFFFFu, pg, 2 * (it & 15)), p1 = __shfl_sync(0xFFFFFFFFu, pg, 2 * (it & 15) + 1);
+            ok_now = (ok_now & ~(3u << (2 * st))) | ((unsigned)((p0 >= 0) | ((p1 >= 0) << 1)) << (2 * st));
+            if (it < its) {
+                const int r0 = (tok0 + it * kUnit) / kBlk;
+                const uint8_t *s0 = a.pool + p0 * p.page_stride + ((long long)kvh * rpp + r0 % rpp) * RB;
+                const uint8_t *s1 = a.pool + p1 * p.page_stride + ((long long)kvh * rpp + (r0 + 1) % rpp) * RB - RB;
+                const unsigned dst = ring_s + st * TB;
+#pragma unroll
+                for (int c = 0; c < TB / 512; c++) {
+                    const int o = (c * 32 + lane) * 16;
+                    if (o < RB ? p0 >= 0 : p1 >= 0) copy16(dst + o, (o < RB ? s0 : s1) + o);
+                }
+                if (TB % 512 && lane < TB % 512 / 16) {
+                    const int o = (TB / 512 * 32 + lane) * 16;
+                    if (p1 >= 0) copy16(dst + o, s1 + o);
+                }
+            }
+            copy_commit();
+        };
+#pragma unroll
+        for (int i = 0; i < ST - 1; i++) issue(i);
+
+        // ---- queries: column n = 8 nt + g of the fragment, channels 16j + 4t + 0..3 of step j, under 2^kq of the column's own
+        unsigned q[NT][KS][2];
+        float qsum[NT][NG][2], qscale[NT][2];
+        int hi[NT][2], lo[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            const int col = ct * COLS + nt * 8 + g, row = col / a.R, h = kvh * a.R + col % a.R;
+            const bool have = row < s.n;
+            const uint16_t *src = a.q + (long long)(s.first + row) * a.q_stride + (long long)h * D + 4 * t;
+            float top = 0.0f;
+            unsigned raw[KS][2];
+#pragma unroll
+            for (int j = 0; j < KS; j++) {
+                raw[j][0] = raw[j][1] = 0;
+                if (have) {
+                    if (a.q_vec) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(src + 16 * j);
+                        raw[j][0] = w.x;
+                        raw[j][1] = w.y;
+                    } else {
+                        raw[j][0] = src[16 * j] | ((unsigned)src[16 * j + 1] << 16);
+                        raw[j][1] = src[16 * j + 2] | ((unsigned)src[16 * j + 3] << 16);
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+                    top = fmaxf(top, fmaxf(fabsf(bits_to_float<BF>(raw[j][i] & 0xFFFFu)),
+                                           fabsf(bits_to_float<BF>(raw[j][i] >> 16))));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+            // the column's largest goes to [2^13, 2^14)
+            int kq = top > 0.0f ? 13 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
+            kq = kq > 120 ? 120 : kq;
+            const float f = pow2f(kq);
+            float sums[NG];
+#pragma unroll
+            for (int i = 0; i < NG; i++) sums[i] = 0.0f;
+#pragma unroll
+            for (int j = 0; j < KS; j++) {
+                float x[4] = {bits_to_float<BF>(raw[j][0] & 0xFFFFu), bits_to_float<BF>(raw[j][0] >> 16),
+                              bits_to_float<BF>(raw[j][1] & 0xFFFFu), bits_to_float<BF>(raw[j][1] >> 16)};
+                q[nt][j][0] = pack_half(x[0] * f, x[1] * f);
+                q[nt][j][1] = pack_half(x[2] * f * 0.0625f, x[3] * f * 0.0625f);  // meets codes 16 times too large
+                const float2 y = __half22float2(*reinterpret_cast<__half2 *>(&q[nt][j][0]));
+                const float2 z = __half22float2(*reinterpret_cast<__half2 *>(&q[nt][j][1]));
+                sums[16 * j / G] += (y.x + y.y) + 16.0f * (z.x + z.y);
+            }
+#pragma unroll
+            for (int i = 0; i < NG; i++) {
+                sums[i] += __shfl_xor_sync(0xFFFFFFFFu, sums[i], 1);
+                sums[i] += __shfl_xor_sync(0xFFFFFFFFu, sums[i], 2);
+            }
+            const float back = a.scale * kLog2e * pow2f(24 - kq > 127 ? 127 : 24 - kq);
+            // to the accumulators' columns 2t, 2t + 1
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                const int src_lane = (2 * t + c) * 4;
+#pragma unroll
+                for (int i = 0; i < NG; i++)
+                    qsum[nt][i][c] = __shfl_sync(0xFFFFFFFFu, sums[i], src_lane) * 5.9604644775390625e-8f;  // 2^-24
+                qscale[nt][c] = __shfl_sync(0xFFFFFFFFu, back, src_lane);
+                const int r = (ct * COLS + nt * 8 + 2 * t + c) / a.R;
+                const long long pos = pos0 + r;
+                hi[nt][c] = r < s.n ? (int)(pos < s.len ? pos : (long long)s.len - 1) : -1;
+                lo[nt][c] = r < s.n && a.window && pos + 1 > a.window ? (int)(pos + 1 - a.window) : 0;
+            }
+        }
+        int hi_min = 0x7FFFFFFF, lo_max = 0;  // tokens that every column sees
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                if (ct * COLS + nt * 8 + 2 * t + c < s.n * a.R) hi_min = min(hi_min, hi[nt][c]);
+                lo_max = max(lo_max, lo[nt][c]);
+            }
+        hi_min = __reduce_min_sync(0xFFFFFFFFu, hi_min);
+        lo_max = __reduce_max_sync(0xFFFFFFFFu, lo_max);
+
+        float o[NT][KS][4], m[NT][2], l[NT][2];
+        unsigned bits[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+            for (int j = 0; j < KS; j++) o[nt][j][0] = o[nt][j][1] = o[nt][j][2] = o[nt][j][3] = 0.0f;
+            m[nt][0] = m[nt][1] = -INFINITY;
+            l[nt][0] = l[nt][1] = 0.0f;
+            bits[nt][0] = bits[nt][1] = 0;
+        }
+        int sig = kSigMin;  // every |V^| seen is below 2^(sig + 1)
+
+        for (int it = 0; it < its; it++) {
+            copy_wait<ST - 2>();
+            __syncwarp();
+            const int st = it % ST;
+            const uint8_t *tile = ring + st * TB;
+            const int tok = tok0 + it * kUnit;
+            const unsigned okr = (ok_now >> (2 * st)) & 3u;
+            issue(it + ST - 1);  // into the stage of the tile before, which every lane has left
+            const bool plain = okr == 3u && tok >= lo_max && tok + kTile - 1 <= hi_min;
+            if (okr != 0u && tok < s.len) {
+                float sc[2][NT][4];
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    const uint8_t *rec = tile + r * RB;
+                    unsigned ka[W], kb[W];
+#pragma unroll
+                    for (int i = 0; i < W; i++) {
+                        // vector loads of the lane's chunk: tokens g and 8 + g
+                        if (W == 2) {
+                            if (i == 0) {
+                                const uint2 x = *reinterpret_cast<const uint2 *>(rec + lane * (D / 8));
+                                const uint2 y = *reinterpret_cast<const uint2 *>(rec + 4 * D + lane * (D / 8));
+                                ka[0] = x.x, ka[1] = x.y, kb[0] = y.x, kb[1] = y.y;
+                            }
+                        } else if (i % 4 == 0) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(rec + lane * (D / 8) + 4 * i);
+                            const uint4 y = *reinterpret_cast<const uint4 *>(rec + 4 * D + lane * (D / 8) + 4 * i);
+                            ka[i] = x.x, ka[i + 1] = x.y, ka[i + 2] = x.z, ka[i + 3] = x.w;
+                            kb[i] = y.x, kb[i + 1] = y.y, kb[i + 2] = y.z, kb[i + 3] = y.w;
+                        }
+                    }
+                    const unsigned *pk = reinterpret_cast<const unsigned *>(rec + R::kPK);
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) sc[r][nt][0] = sc[r][nt][1] = sc[r][nt][2] = sc[r][nt][3] = 0.0f;
+#pragma unroll
+                    for (int i = 0; i < NG; i++) {
+                        float dot[NT][4];
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++) dot[nt][0] = dot[nt][1] = dot[nt][2] = dot[nt][3] = 0.0f;
+#pragma unroll
+                        for (int w = i * G / 32; w < (i + 1) * G / 32; w++) {
+                            const unsigned x = ka[w], y = kb[w], xs = x >> 8, ys = y >> 8;
+#pragma unroll
+                            for (int nt = 0; nt < NT; nt++) {
+                                mma(dot[nt], x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u,
+                                    q[nt][2 * w][0], q[nt][2 * w][1]);
+                                mma(dot[nt], xs & 0x000F000Fu, ys & 0x000F000Fu, xs & 0x00F000F0u, ys & 0x00F000F0u,
+                                    q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
+                            }
+                        }
+                        const unsigned pa = pk[g * NG + i], pb = pk[(8 + g) * NG + i];
+                        const float s0 = bits_to_float<BF>(pa & 0xFFFFu), m0 = bits_to_float<BF>(pa >> 16);
+                        const float s1 = bits_to_float<BF>(pb & 0xFFFFu), m1 = bits_to_float<BF>(pb >> 16);
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+                            for (int c = 0; c < 2; c++) {
+                                sc[r][nt][c] = fmaf(s0, dot[nt][c], fmaf(m0, qsum[nt][i][c], sc[r][nt][c]));
+                                sc[r][nt][2 + c] = fmaf(s1, dot[nt][2 + c], fmaf(m1, qsum[nt][i][c], sc[r][nt][2 + c]));
+                            }
+                        }
+                    }
+                }
+                // ---- base-2 scores, hidden ones -inf
+#pragma unroll
+                for (int r = 0; r < 2; r++)
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int c = 0; c < 4; c++) {
+                            sc[r][nt][c] *= qscale[nt][c & 1];
+                            if (!plain) {
+                                const int at = tok + r * kBlk + (c >> 1) * 8 + g;
+                                if (!((okr >> r) & 1u) || at > hi[nt][c & 1] || at < lo[nt][c & 1])
+                                    sc[r][nt][c] = -INFINITY;
+                            }
+                        }
+                // ---- value parameters of tokens 2t, 2t + 1, 8 + 2t, 8 + 2t + 1, this lane's group; sigma
+                float vs[2][4], vm[2][4];
+                float big = 0.0f;
+                bool odd = false;
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    const unsigned *pv = reinterpret_cast<const unsigned *>(tile + r * RB + R::kPV) + g * (D / 8) / G;
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const int tk = (i >> 1) * 8 + 2 * t + (i & 1);
+                        const unsigned w = pv[tk * NG];
+                        float sv = bits_to_float<BF>(w & 0xFFFFu), mv = bits_to_float<BF>(w >> 16);
+                        const bool fine = fabsf(sv) <= 3.402823466e38f && fabsf(mv) <= 3.402823466e38f;
+                        const bool held = ((okr >> r) & 1u) && tok + r * kBlk + tk < s.len;
+                        odd |= held && !fine;
+                        if (!fine || !held) sv = mv = 0.0f;
+                        vs[r][i] = sv;
+                        vm[r][i] = mv;
+                        big = fmaxf(big, fmaxf(fabsf(mv), fabsf(fmaf(15.0f, sv, mv))));
+                    }
+                }
+                const unsigned bu = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(big, 3.402823466e38f)));
+                const int e = max((int)(bu >> 23) - 127, kSigMin);
+                // ---- maxima; they follow the scores in steps of at least 6, so that accumulators are rarely rescaled
+                float mx[NT][2];
+                bool change = e > sig;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int c = 0; c < 2; c++) {
+                        float x = fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]), fmaxf(sc[1][nt][c], sc[1][nt][2 + c]));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                        mx[nt][c] = x > m[nt][c] + 6.0f ? x : m[nt][c];
+                        change |= mx[nt][c] != m[nt][c];
+                    }
+                if (__any_sync(0xFFFFFFFFu, change)) {
+                    const int ns = max(e, sig);
+                    const float fs = sig - ns < -126 ? 0.0f : pow2f(sig - ns);
+                    sig = ns;
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int c = 0; c < 2; c++) {
+                            const float f = m[nt][c] == mx[nt][c] ? 1.0f : exp2_approx(m[nt][c] - mx[nt][c]);
+                            m[nt][c] = mx[nt][c];
+                            l[nt][c] *= f;
+#pragma unroll
+                            for (int j = 0; j < KS; j++) {
+                                o[nt][j][c] *= f * fs;
+                                o[nt][j][2 + c] *= f * fs;
+                            }
+                        }
+                }
+                if (__any_sync(0xFFFFFFFFu, odd)) {  // groups that are not finite: remembered for the columns that see them
+#pragma unroll
+                    for (int r = 0; r < 2; r++)
+                        for (int i = 0; i < NG; i++)
+#pragma unroll
+                            for (int k = 0; k < 2; k++) {
+                                const unsigned w = reinterpret_cast<const unsigned *>(tile + r * RB + R::kPV)[(8 * k + g) * NG + i];
+                                if (!(fabsf(bits_to_float<BF>(w & 0xFFFFu)) <= 3.402823466e38f))
+#pragma unroll
+                                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                                        for (int c = 0; c < 2; c++)
+                                            if (sc[r][nt][2 * k + c] != -INFINITY) bits[nt][c] |= 1u << i;
+                            }
+                }
+                // ---- weights, values
+                // V^ 2^(-7 - sig), within (-2^-6, 2^-6): c 2^-24 times s 2^(17 - sig), below 2^16 since 15 s < 2^(sig + 2)
+                const float fs = pow2f(17 - sig);
+#pragma unroll
+                for (int r = 0; r < 2; r++) {
+                    unsigned pb[NT][2];
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) {
+                        float pr[4];
+#pragma unroll
+                        for (int c = 0; c < 4; c++) {
+                            const float mm = m[nt][c & 1] == -INFINITY ? 0.0f : m[nt][c & 1];
+                            pr[c] = exp2_approx(sc[r][nt][c] - mm);
+                            l[nt][c & 1] += pr[c];
+                        }
+                        pb[nt][0] = transposed(pack_half(pr[0], pr[1]));
+                        pb[nt][1] = transposed(pack_half(pr[2], pr[3]));
+                    }
+                    unsigned s1[2], s16[2], mm2[2];
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        const float x = vs[r][2 * k] * fs, y = vs[r][2 * k + 1] * fs;
+                        s1[k] = pack_half(x, y);
+                        s16[k] = pack_half(x * 0.0625f, y * 0.0625f);
+                        mm2[k] = pack_half(vm[r][2 * k] * 5.9604644775390625e-8f * fs,
+                                           vm[r][2 * k + 1] * 5.9604644775390625e-8f * fs);
+                    }
+                    const uint8_t *rec = tile + r * RB + R::kV;
+                    constexpr int VW = D / 64;  // words of a token's piece
+                    unsigned va[2][2 * VW > 4 ? 2 * VW : 4];
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        if (VW == 1) {
+                            const uint2 x = *reinterpret_cast<const uint2 *>(rec + k * 4 * D + lane * (D / 8));
+                            va[k][0] = x.x, va[k][1] = x.y;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < 2 * VW; i += 4) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(rec + k * 4 * D + lane * (D / 8) + 4 * i);
+                                va[k][i] = x.x, va[k][i + 1] = x.y, va[k][i + 2] = x.z, va[k][i + 3] = x.w;
+                            }
+                        }
+                    }
+#pragma unroll
+                    for (int w = 0; w < VW; w++)
+#pragma unroll
+                        for (int y = 0; y < 2; y++) {
+                            // channels 8w + 4y + 0..3 of the piece, tokens (2t, 2t + 1) of either half side by side
+                            unsigned x0 = __byte_perm(va[0][w], va[0][VW + w], y ? 0x7632 : 0x5410);
+                            unsigned x1 = __byte_perm(va[1][w], va[1][VW + w], y ? 0x7632 : 0x5410);
+#pragma unroll
+                            for (int z = 0; z < 2; z++) {
+                                const unsigned a0 = fma_half(x0 & 0x000F000Fu, s1[0], mm2[0]);
+                                const unsigned a1 = fma_half(x0 & 0x00F000F0u, s16[0], mm2[0]);
+                                const unsigned a2 = fma_half(x1 & 0x000F000Fu, s1[1], mm2[1]);
+                                const unsigned a3 = fma_half(x1 & 0x00F000F0u, s16[1], mm2[1]);
+#pragma unroll
+                                for (int nt = 0; nt < NT; nt++)
+                                    mma(o[nt][(w * 2 + y) * 2 + z], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+                                x0 >>= 8;
+                                x1 >>= 8;
+                            }
+                        }
+                }
+            }
+        }
+        copy_wait<0>();
+
+        // ---- join the warps: accumulators through shared memory in the ring's place
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+#pragma unroll
+                for (int x = 4; x <= 16; x <<= 1) {
+                    l[nt][c] += __shfl_xor_sync(0xFFFFFFFFu, l[nt][c], x);
+                    bits[nt][c] |= __shfl_xor_sync(0xFFFFFFFFu, bits[nt][c], x);
+                }
+                if (g == 0) {
+                    s_m[warp][nt * 8 + 2 * t + c] = m[nt][c];
+                    s_l[warp][nt * 8 + 2 * t + c] = l[nt][c];
+                    s_bits[warp][nt * 8 + 2 * t + c] = bits[nt][c];
+                }
+            }
+        __syncthreads();  // every warp is done with its ring
+        // o[w][col][D + 4]: the accumulators' own column order, channel g*D/8 + 2*tile + {0, 1}
+        constexpr int OS = D + 4;
+        float *so = reinterpret_cast<float *>(smem);
+        static_assert(kWarps * COLS * OS * 4 <= ring_bytes<D, G>(), "accumulators fit the ring");
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+            for (int j = 0; j < KS; j++)
+#pragma unroll
+                for (int c = 0; c < 2; c++)
+                    *reinterpret_cast<float2 *>(so + (warp * COLS + nt * 8 + 2 * t + c) * OS + g * (D / 8) + 2 * j) =
+                        make_float2(o[nt][j][c], o[nt][j][2 + c]);
+        if (lane == 0) s_sigma[warp] = pow2f(sig);
+        __syncthreads();
+
+        const bool whole = ua == 0 && ub == s.units;
+        const int ncols = min(COLS, s.n * a.R - ct * COLS);
+        // slot of this CTA's part: 0 where the item began in an earlier CTA, else 1
+        float *part = partials + ((long long)blockIdx.x * 2 + (ua == 0 ? 1 : 0)) * PF;
+        constexpr int Q4 = D / 4;
+        for (int i = threadIdx.x; i < ncols * Q4; i += kThreads) {
+            const int c = i / Q4, d = (i % Q4) * 4;
+            float top = s_m[0][c];
+#pragma unroll
+            for (int w = 1; w < kWarps; w++) top = fmaxf(top, s_m[w][c]);
+            float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+            float tl = 0.0f;
+            unsigned bb = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) {
+                const float f = s_m[w][c] == -INFINITY ? (s_l[w][c] == 0.0f ? 0.0f : s_l[w][c]) : exp2_approx(s_m[w][c] - top);
+                tl += s_l[w][c] * f;
+                const float fo = 128.0f * f, up = s_sigma[w];
+                const float4 y = *reinterpret_cast<const float4 *>(so + (w * COLS + c) * OS + d);
+                if (s_m[w][c] != -INFINITY || s_l[w][c] != 0.0f) {
+                    x.x += y.x * fo * up;
+                    x.y += y.y * fo * up;
+                    x.z += y.z * fo * up;
+                    x.w += y.w * fo * up;
+                }
+                bb |= s_bits[w][c];
+            }
+            if (whole) {
+                put_out<D, G, BF>(a, s, kvh, ct * COLS + c, d, x, top, tl, bb);
+            } else {
+                *reinterpret_cast<float4 *>(part + c * D + d) = x;
+                if (d == 0) {
+                    part[COLS * D + 3 * c] = top;
+                    part[COLS * D + 3 * c + 1] = tl;
+                    part[COLS * D + 3 * c + 2] = __uint_as_float(bb);
+                }
+            }
+        }
+        if (!whole) {
+            // the CTAs that share the item are those whose ranges meet it
+            const long long first_cta = cta_of(item_u0, total, grid), last_cta = cta_of(item_u1 - 1, total, grid);
+            const int count = (int)(last_cta - first_cta + 1);
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                // tickets: one a CTA; the item's is that of the first CTA that has a part of it, which ends there
+                const unsigned was = atomicAdd(tickets + first_cta, 1u);
+                s_last = was == (unsigned)(count - 1);
+                if (s_last) tickets[first_cta] = 0;
+            }
+            __syncthreads();
+            if (s_last) {
+                __threadfence();
+                for (int i = threadIdx.x; i < ncols * Q4; i += kThreads) {
+                    const int c = i / Q4, d = (i % Q4) * 4;
+                    float top = -INFINITY, tl = 0.0f;
+                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+                    unsigned bb = 0;
+                    for (int k = 0; k < count; k++) {
+                        const float *src = partials + ((first_cta + k) * 2 + (k == 0 ? 1 : 0)) * PF;
+                        const float pm = __ldcg(src + COLS * D + 3 * c), pl = __ldcg(src + COLS * D + 3 * c + 1);
+                        const unsigned pbits = __float_as_uint(__ldcg(src + COLS * D + 3 * c + 2));
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + c * D + d));
+                        if (pm == -INFINITY && pl == 0.0f) continue;
+                        const float nt_ = fmaxf(top, pm);
+                        const float f0 = top == -INFINITY ? (tl == 0.0f ? 0.0f : 1.0f) : exp2_approx(top - nt_);
+                        const float f1 = pm == -INFINITY ? 1.0f : exp2_approx(pm - nt_);
+                        top = nt_;
+                        tl = tl * f0 + pl * f1;
+                        x.x = x.x * f0 + y.x * f1;
+                        x.y = x.y * f0 + y.y * f1;
+                        x.z = x.z * f0 + y.z * f1;
+                        x.w = x.w * f0 + y.w * f1;
+                        bb |= pbits;
+                    }
+                    put_out<D, G, BF>(a, s, kvh, ct * COLS + c, d, x, top, tl, bb);
+                }
+            }
+        }
+        __syncthreads();  // the ring is free again
+        u += its;
     }
-    if (a.lse && threadIdx.x == 0) a.lse[(long long)row * a.Hq + h] = top == -INFINITY ? top : top + logf(total);
+}
+
+// CTAs that fill the GPU; the workspace's layout allows for kMaxGrid of them.
+constexpr int kMaxGrid = 1024;
+
+template <auto kKernel, int kBytes>
+cudaError_t launch_filling(const Kv4 &p, const Kv4Attend &a, cudaStream_t s) {
+    static int per_sm = 0;  // the same on every device of this architecture
+    if (per_sm == 0) {
+        cudaError_t e = cudaFuncSetAttribute(kKernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kBytes);
+        int n = 0;
+        if (e == cudaSuccess) e = cudaOccupancyMaxActiveBlocksPerMultiprocessor(&n, kKernel, kThreads, kBytes);
+        if (e != cudaSuccess) return e;
+        per_sm = n > 0 ? n : 1;
+    }
+    int grid = per_sm * device_sm_count();
+    if (grid > kMaxGrid) grid = kMaxGrid;
+    if (grid < 1) return cudaErrorInvalidDevice;
+    kKernel<<<grid, kThreads, kBytes, s>>>(p, a);
+    return cudaGetLastError();
+}
+
+template <int D, int G, int NT>
+cudaError_t step_nt(const Kv4 &p, const Kv4Attend &a, cudaStream_t s) {
+    constexpr int bytes = ring_bytes<D, G>();
+    if (p.dtype == CG_DT_BF16) return launch_filling<k_kv4_step<D, G, NT, true>, bytes>(p, a, s);
+    return launch_filling<k_kv4_step<D, G, NT, false>, bytes>(p, a, s);
 }
 
 template <int D, int G>
 cudaError_t step_dg(const Kv4 &p, const Kv4Attend &a, cudaStream_t s) {
-    const long long n = (long long)p.rows * a.Hq;
-    if (p.dtype == CG_DT_BF16) k_kv4_rows<D, G, true><<<(unsigned)n, 128, 0, s>>>(p, a);
-    else k_kv4_rows<D, G, false><<<(unsigned)n, 128, 0, s>>>(p, a);
-    return cudaGetLastError();
+    if constexpr (D < 256) {
+        if ((long long)p.max_rows * a.R > 8) return step_nt<D, G, 2>(p, a, s);
+    }
+    return step_nt<D, G, 1>(p, a, s);
 }
 
 }  // namespace
+
+uint64_t kv4_ticket_bytes() { return 4ull * kMaxGrid; }
+
+uint64_t kv4_step_workspace_bytes(const Kv4 &p) {
+    const uint64_t cols = p.D < 256 ? 16 : 8;
+    return kv4_ticket_bytes() + 2ull * kMaxGrid * 4 * (cols * p.D + 3 * cols);
+}
 
 cudaError_t launch_kv4_step(const Kv4 &p, const Kv4Attend &a, cudaStream_t s) {
     switch (p.D * 1000 + p.G) {
