@@ -23,8 +23,10 @@ __all__ = ["Cache4", "Batch4"]
 _DTYPES = {torch.float16: capi.CG_DT_F16, torch.bfloat16: capi.CG_DT_BF16}
 
 
-def _stream(stream: torch.cuda.Stream | None) -> int:
-    return (stream if stream is not None else torch.cuda.current_stream()).cuda_stream
+# The handle of a device's current stream: what torch.cuda.current_stream(i).cuda_stream gives, without
+# the stream object (a step's calls take microseconds, most of them on the host).
+_current = torch._C._cuda_getCurrentRawStream
+_capturing = torch._C._cuda_isCurrentStreamCapturing
 
 
 class Batch4:
@@ -103,44 +105,55 @@ class Cache4:
             raise ValueError("pool must be 16-byte aligned")
         self.pool = pool
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
-        self._pool, self._status = pool.data_ptr(), self.status.data_ptr()
+        self._pool, self._status, self._device = pool.data_ptr(), self.status.data_ptr(), pool.get_device()
+        self._at = pool.device
+        one = capi.cg_kv4_batch()
+        self._ws_bytes = int(self._lib.cg_kv4_attention_workspace_bytes(self._ref, C.byref(one), H))
         self._ws: dict[int, torch.Tensor] = {}  # attention's workspace of each stream
+        # arguments that every call repeats, as the binding takes them
+        self._a = (C.c_void_p(self._pool), self._ref)
+        self._fn = {n: getattr(self._lib, "cg_kv4_" + n) for n in ("write", "read", "attention")}
+        self._scale = D ** -0.5
 
-    def _workspace(self, stream: int, need: int) -> torch.Tensor:
+    def _stream(self, stream) -> int:
+        return _current(self._device) if stream is None else stream.cuda_stream
+
+    def _workspace(self, stream: int) -> torch.Tensor:
         """The stream's workspace. Calls on one stream follow one another and may
         share it; a captured call, which may be replayed on any, gets its own."""
         ws = self._ws.get(stream)
-        if ws is None or ws.numel() < need or torch.cuda.is_current_stream_capturing():
-            ws = torch.zeros(need, dtype=torch.uint8, device=self.pool.device)
-            if not torch.cuda.is_current_stream_capturing():
+        if ws is None or _capturing():
+            ws = torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self._at)
+            if not _capturing():
                 self._ws[stream] = ws
         return ws
 
     def _kv(self, name, t, batch, layers):
         """Strides (row, layer) of t: [rows, H, D] or [rows, H*D], with a dimension of layers before where there are several."""
-        if t.dtype != self.dtype:
+        if t.dtype is not self.dtype:
             raise TypeError(f"{name} must be {self.dtype}")
-        if t.device != self.pool.device:
+        if t.get_device() != self._device:
             raise ValueError(f"{name} must be on the cache's device")
-        HD = self.H * self.D
-        lead = () if layers is None else (layers,)
-        if t.shape == (*lead, batch.rows, HD):
-            ok = t.stride(-1) == 1
-        elif t.shape == (*lead, batch.rows, self.H, self.D):
-            ok = t.stride(-1) == 1 and (t.stride(-2) == self.D or self.H == 1)
-        else:
+        shape, stride = t.shape, t.stride()
+        n = 0 if layers is None else 1
+        if shape[:n + 1] != (batch.rows,) if n == 0 else shape[:2] != (layers, batch.rows):
             ok = False
+        elif len(shape) == n + 2:
+            ok = shape[-1] == self.H * self.D and stride[-1] == 1
+        else:
+            ok = shape[n + 1:] == (self.H, self.D) and stride[-1] == 1 and (stride[-2] == self.D or self.H == 1)
         if not ok:
-            raise ValueError(f"{name} must be {[*lead, batch.rows, HD]} (or with [H, D] last), a row's channels contiguous")
-        n = len(lead)
-        return t.stride(n), t.stride(0) if n else 0
+            want = [batch.rows] if layers is None else [layers, batch.rows]
+            raise ValueError(f"{name} must be {want + [self.H * self.D]} (or with [H, D] last), a row's channels contiguous")
+        return stride[n], stride[0] if n else 0
 
     def _write(self, k, v, batch, layer, layers, stream):
         ks, kl = self._kv("k", k, batch, layers)
         vs, vl = self._kv("v", v, batch, layers)
-        capi.check(self._lib.cg_kv4_write(self._pool, self._ref, batch._ref, layer, 1 if layers is None else layers,
-                                          k.data_ptr(), v.data_ptr(), ks, vs, kl, vl, self._status, _stream(stream)),
-                   "cg_kv4_write")
+        code = self._fn["write"](*self._a, batch._ref, layer, 1 if layers is None else layers, k.data_ptr(), v.data_ptr(),
+                                 ks, vs, kl, vl, self._status, self._stream(stream))
+        if code:
+            capi.check(code, "cg_kv4_write")
 
     def write(self, k: torch.Tensor, v: torch.Tensor, batch: Batch4, layer: int = 0, stream=None) -> None:
         """Quantise the batch's rows of one layer into their slots. k, v:
@@ -158,7 +171,11 @@ class Cache4:
             raise TypeError(f"a read gives {self.dtype} or torch.float32")
         shape = (batch.rows, self.H, self.D) if layers is None else (layers, batch.rows, self.H * self.D)
         if out is None:
-            k, v = (torch.empty(shape, dtype=dtype, device=self.pool.device) for _ in range(2))
+            if stream is None:
+                k, v = (torch.empty(shape, dtype=dtype, device=self._at), torch.empty(shape, dtype=dtype, device=self._at))
+            else:  # memory for the call belongs to its stream
+                with torch.cuda.stream(stream):
+                    k, v = (torch.empty(shape, dtype=dtype, device=self._at) for _ in range(2))
         else:
             k, v = out
             if k.dtype != dtype or v.dtype != dtype or k.device != self.pool.device or v.device != k.device:
@@ -167,9 +184,12 @@ class Cache4:
                     (layers is None and self.H > 1 and k.stride(1) != self.D):
                 raise ValueError(f"out must be two tensors {list(shape)} of equal strides, a row's channels contiguous")
         n = 0 if layers is None else 1
-        capi.check(self._lib.cg_kv4_read(self._pool, self._ref, batch._ref, layer, 1 if layers is None else layers,
-                                         int(dtype == torch.float32), k.data_ptr(), v.data_ptr(), k.stride(n),
-                                         k.stride(0) if n else 0, self._status, _stream(stream)), "cg_kv4_read")
+        stride = k.stride()
+        code = self._fn["read"](*self._a, batch._ref, layer, 1 if layers is None else layers, dtype is torch.float32,
+                                k.data_ptr(), v.data_ptr(), stride[n], stride[0] if n else 0, self._status,
+                                self._stream(stream))
+        if code:
+            capi.check(code, "cg_kv4_read")
         return k, v
 
     def read(self, batch: Batch4, layer: int = 0, dtype: torch.dtype | None = None, out=None, stream=None):
@@ -192,29 +212,38 @@ class Cache4:
         D**-0.5. -> out [rows, Hq, D], with return_lse also the natural
         log-sum-exp of the scaled scores, float32 [rows, Hq] (-inf, and out 0,
         where a row sees nothing)."""
-        if q.dtype != self.dtype:
+        if q.dtype is not self.dtype:
             raise TypeError(f"q must be {self.dtype}")
-        if q.device != self.pool.device:
+        if q.get_device() != self._device:
             raise ValueError("q must be on the cache's device")
-        D = self.D
-        if q.dim() != 3 or q.shape[0] != batch.rows or q.shape[2] != D or q.stride(2) != 1 or \
-                (q.shape[1] > 1 and q.stride(1) != D):
+        D, shape, stride = self.D, q.shape, q.stride()
+        if len(shape) != 3 or shape[0] != batch.rows or shape[2] != D or stride[2] != 1 or \
+                (stride[1] != D and shape[1] > 1):
             raise ValueError(f"q must be [{batch.rows}, Hq, {D}], a row's channels contiguous")
-        Hq = q.shape[1]
+        Hq = shape[1]
         if Hq == 0 or Hq % self.H:
             raise ValueError(f"the query heads ({Hq}) must be a multiple of the cache's {self.H}")
-        with torch.cuda.stream(stream):  # memory for the call belongs to its stream
-            if out is None:
-                out = torch.empty((batch.rows, Hq, D), dtype=q.dtype, device=q.device)
-            elif out.dtype != q.dtype or out.shape != q.shape or out.device != q.device or out.stride(2) != 1 or \
-                    (Hq > 1 and out.stride(1) != D):
-                raise ValueError("out must be like q")
-            lse = torch.empty((batch.rows, Hq), dtype=torch.float32, device=q.device) if return_lse else None
-            need = int(self._lib.cg_kv4_attention_workspace_bytes(self._ref, batch._ref, Hq))
-            ws = self._workspace(_stream(stream), need)
-        capi.check(self._lib.cg_kv4_attention(
-            self._pool, self._ref, batch._ref, layer, Hq, q.data_ptr(), q.stride(0),
-            D ** -0.5 if scale is None else scale, window, out.data_ptr(), out.stride(0),
-            None if lse is None else lse.data_ptr(), ws.data_ptr(), need, self._status, _stream(stream)),
-            "cg_kv4_attention")
+        if stream is not None:  # memory for the call belongs to its stream
+            with torch.cuda.stream(stream):
+                return self._attend(q, batch, layer, scale, window, return_lse, out, Hq, stride[0])
+        return self._attend(q, batch, layer, scale, window, return_lse, out, Hq, stride[0])
+
+    def _attend(self, q, batch, layer, scale, window, return_lse, out, Hq, q_stride):
+        if out is None:
+            out = torch.empty(q.shape, dtype=q.dtype, device=self._at)
+            out_stride = Hq * self.D
+        elif out.dtype != q.dtype or out.shape != q.shape or out.device != q.device or out.stride(2) != 1 or \
+                (Hq > 1 and out.stride(1) != self.D):
+            raise ValueError("out must be like q")
+        else:
+            out_stride = out.stride(0)
+        lse = torch.empty((batch.rows, Hq), dtype=torch.float32, device=self._at) if return_lse else None
+        stream = _current(self._device)
+        ws = self._workspace(stream)
+        code = self._fn["attention"](
+            *self._a, batch._ref, layer, Hq, q.data_ptr(), q_stride, self._scale if scale is None else scale, window,
+            out.data_ptr(), out_stride, None if lse is None else lse.data_ptr(), ws.data_ptr(), self._ws_bytes,
+            self._status, stream)
+        if code:
+            capi.check(code, "cg_kv4_attention")
         return (out, lse) if return_lse else out

@@ -32,39 +32,99 @@ __device__ __forceinline__ unsigned code_of(float x, float lo, float s) {
     return (unsigned)__float2int_rn(fminf(__fdiv_rn(__fsub_rn(x, lo), s), 15.0f));
 }
 
-// fminf and fmaxf drop NaNs; the running range keeps them.
-__device__ __forceinline__ void widen(float &lo, float &hi, float a, float b) {
-    lo = a < lo || a != a ? a : lo;
-    hi = b > hi || b != b ? b : hi;
+// Two 16-bit values side by side: the lesser, the greater of each, NaNs kept.
+template <bool BF>
+__device__ __forceinline__ unsigned min_pair(unsigned a, unsigned b) {
+    unsigned y;
+    if (BF) asm("min.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    else asm("min.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
+template <bool BF>
+__device__ __forceinline__ unsigned max_pair(unsigned a, unsigned b) {
+    unsigned y;
+    if (BF) asm("max.NaN.bf16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    else asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
 }
 
-// 4 values from p; VEC: p is 8-byte aligned.
-template <bool BF, bool VEC>
-__device__ __forceinline__ void load4(const uint16_t *p, float *x) {
-    if (VEC) {
-        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
-        x[0] = bits_to_float<BF>(w.x & 0xFFFFu);
-        x[1] = bits_to_float<BF>(w.x >> 16);
-        x[2] = bits_to_float<BF>(w.y & 0xFFFFu);
-        x[3] = bits_to_float<BF>(w.y >> 16);
-    } else {
+// The range of a group: N pairs of this lane, and those of the lanes `from`, 2 from, ... `to` / 2 away.
+template <bool BF, int N>
+__device__ __forceinline__ void range_of(const unsigned *x, int from, int to, float &lo, float &hi) {
+    unsigned a = x[0], b = x[0];
 #pragma unroll
-        for (int i = 0; i < 4; i++) x[i] = bits_to_float<BF>(__ldg(p + i));
+    for (int i = 1; i < N; i++) {
+        a = min_pair<BF>(a, x[i]);
+        b = max_pair<BF>(b, x[i]);
+    }
+#pragma unroll
+    for (int o = from; o < to; o <<= 1) {
+        a = min_pair<BF>(a, __shfl_xor_sync(0xFFFFFFFFu, a, o));
+        b = max_pair<BF>(b, __shfl_xor_sync(0xFFFFFFFFu, b, o));
+    }
+    a = min_pair<BF>(a, a >> 16);
+    b = max_pair<BF>(b, b >> 16);
+    lo = bits_to_float<BF>(a & 0xFFFFu);
+    hi = bits_to_float<BF>(b & 0xFFFFu);
+}
+
+// The codes of N pairs of one group into words: pair j's go to nibbles nib(j), nib2(j) of word j / 4.
+// rint((x - lo) / s) without a division: y = (x - lo) (1/s) is within 2^-19 of the quotient, so its nearest
+// whole number is the quotient's unless y lies that close to halfway; then (or where s is none, or so small
+// that its own rounding let the quotient pass 15) the eight values of the word are divided.
+template <bool BF, int N, typename Nib, typename Nib2>
+__device__ __forceinline__ void codes_of(const unsigned *x, float lo, float hi, float s, unsigned *words, Nib nib,
+                                         Nib2 nib2) {
+    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: y + kMagic has y's nearest whole number in its last bits
+    const bool plain = s > 1e-30f && hi - lo <= 15.4f * s;  // 1/s far from its own limits
+    const float r = __fdiv_rn(1.0f, s);
+#pragma unroll
+    for (int i = 0; i < N / 4; i++) {
+        unsigned w = 0, sub = 0;
+        float far = 0.0f;
+#pragma unroll
+        for (int j = 0; j < 8; j++) {
+            const unsigned pair = x[4 * i + j / 2];
+            const int at = 4 * (j & 1 ? nib2(j / 2) : nib(j / 2));
+            const float d = __fsub_rn(bits_to_float<BF>(j & 1 ? pair >> 16 : pair & 0xFFFFu), lo);
+            const float n = __fmaf_rn(d, r, kMagic);
+            far = fmaxf(far, fabsf(__fmaf_rn(d, r, __fsub_rn(kMagic, n))));
+            w += __float_as_uint(n) << at;
+            sub += 0x4B400000u << at;
+        }
+        w -= sub;
+        if (!(plain && far <= 0.49999f)) {
+            w = 0;
+#pragma unroll
+            for (int j = 0; j < 8; j++) {
+                const unsigned pair = x[4 * i + j / 2];
+                w |= code_of(bits_to_float<BF>(j & 1 ? pair >> 16 : pair & 0xFFFFu), lo, s)
+                     << (4 * (j & 1 ? nib2(j / 2) : nib(j / 2)));
+            }
+        }
+        words[i] = w;
     }
 }
-template <bool BF, bool VEC>
-__device__ __forceinline__ void load8(const uint16_t *p, float *x) {
-    if (VEC) {
-        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p));
-        const unsigned u[4] = {w.x, w.y, w.z, w.w};
+
+// N pairs from p; VEC: p is aligned for loads of 8 bytes (N = 2) or 16.
+template <int N, bool VEC>
+__device__ __forceinline__ void load_pairs(const uint16_t *p, unsigned *x) {
+    if (VEC && N == 2) {
+        const uint2 w = __ldg(reinterpret_cast<const uint2 *>(p));
+        x[0] = w.x;
+        x[1] = w.y;
+    } else if (VEC) {
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            x[2 * i] = bits_to_float<BF>(u[i] & 0xFFFFu);
-            x[2 * i + 1] = bits_to_float<BF>(u[i] >> 16);
+        for (int i = 0; i < N; i += 4) {
+            const uint4 w = __ldg(reinterpret_cast<const uint4 *>(p) + i / 4);
+            x[i] = w.x;
+            x[i + 1] = w.y;
+            x[i + 2] = w.z;
+            x[i + 3] = w.w;
         }
     } else {
-        load4<BF, false>(p, x);
-        load4<BF, false>(p + 4, x + 4);
+#pragma unroll
+        for (int i = 0; i < N; i++) x[i] = __ldg(p + 2 * i) | ((unsigned)__ldg(p + 2 * i + 1) << 16);
     }
 }
 
@@ -134,101 +194,72 @@ __global__ void __launch_bounds__(256) k_kv4_write(uint8_t *__restrict__ pool, K
                                                    long long krs, long long vrs, long long kls, long long vls,
                                                    int32_t *status) {
     using R = Rec<D, G>;
-    constexpr int W = D / 32;  // words of a K chunk
+    constexpr int W = D / 32;              // words of a K chunk
+    constexpr int N = D / 8;               // channels of a V piece
+    constexpr int GP = G / N;              // pieces a group
+    static_assert(G >= N, "a piece lies in one group");
     const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
     if (w >= (long long)tiles * p.H * nlayers) return;
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, t = lane & 3, g = lane & 7;
     const Unit u = unit_of(p, w, tiles);
-    bool bad = false;
+    // rows past the end load the last one's values and store nothing: no load waits for the slots
+    const int last = p.rows - 1, row = u.tile * 8 + (lane >> 2);
+    unsigned x[D / 8], z[2][N / 2];  // pairs
+    const uint16_t *src = k + u.layer * kls + min(row, last) * krs + (long long)u.head * D + 4 * t;
+#pragma unroll
+    for (int j = 0; j < D / 16; j++) load_pairs<2, VEC>(src + 16 * j, x + 2 * j);
+#pragma unroll
+    for (int half = 0; half < 2; half++) {
+        src = v + u.layer * vls + min(u.tile * 8 + half * 4 + (lane >> 3), last) * vrs + (long long)u.head * D + g * N;
+        load_pairs<N / 2, VEC>(src, z[half]);
+    }
+    int tok = 0;
+    bool mine, bad = false;
+    const long long at = slot_of(p, row, u.head, layer + u.layer, tok, mine, status);
     {
-        const int row = u.tile * 8 + (lane >> 2), t = lane & 3;
-        int tok = 0;
-        bool mine;
-        const long long at = slot_of(p, row, u.head, layer + u.layer, tok, mine, status);
-        float x[D / 4];
-        const uint16_t *src = k + u.layer * kls + row * krs + (long long)u.head * D + 4 * t;
+        unsigned words[W], params[R::NG];
 #pragma unroll
-        for (int j = 0; j < D / 16; j++) {
-            if (at >= 0) load4<BF, VEC>(src + 16 * j, x + 4 * j);
-            else x[4 * j] = x[4 * j + 1] = x[4 * j + 2] = x[4 * j + 3] = 0.0f;
-        }
-        unsigned words[W];
-#pragma unroll
-        for (int i = 0; i < W; i++) words[i] = 0;
-        unsigned params[R::NG];
-#pragma unroll
-        for (int g = 0; g < R::NG; g++) {
-            float *y = x + g * (G / 4);
-            float lo = y[0], hi = y[0];
-#pragma unroll
-            for (int i = 1; i < G / 4; i++) widen(lo, hi, y[i], y[i]);
-#pragma unroll
-            for (int o = 1; o <= 2; o <<= 1)
-                widen(lo, hi, __shfl_xor_sync(0xFFFFFFFFu, lo, o), __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+        for (int i = 0; i < R::NG; i++) {
+            const unsigned *y = x + i * (G / 8);
+            float lo, hi;
+            range_of<BF, G / 8>(y, 1, 4, lo, hi);
             const float s = group_scale<BF>(lo, hi);
+            // pair j of a word: channels e = 0, 1 (even j) or 2, 3 of step 2w + j / 2
+            codes_of<BF, G / 8>(y, lo, hi, s, words + i * (G / 32), [](int j) { return 2 * (j >> 1) + (j & 1); },
+                                [](int j) { return 4 + 2 * (j >> 1) + (j & 1); });
             if (s != s) {
                 bad |= at >= 0;
                 lo = s;
             }
-            params[g] = float_to_bits<BF>(s) | (float_to_bits<BF>(lo) << 16);
-#pragma unroll
-            for (int i = 0; i < G / 4; i++) {
-                const int j = g * (G / 16) + i / 4, e = i % 4;  // channel 16j + 4t + e
-                const int nib = 4 * (e & 1) + 2 * (j & 1) + (e >> 1);
-                words[j >> 1] |= code_of(y[i], lo, s) << (4 * nib);
-            }
+            params[i] = float_to_bits<BF>(s) | (float_to_bits<BF>(lo) << 16);
         }
         if (at >= 0) {
             uint8_t *rec = pool + at;
             store_words<W>(rec + (tok >> 3) * (4 * D) + (tok & 7) * (D / 2) + t * (D / 8), words);
 #pragma unroll
-            for (int g = 0; g < R::NG; g++)
-                if ((g & 3) == t) *reinterpret_cast<unsigned *>(rec + R::kPK + (tok * R::NG + g) * 4) = params[g];
+            for (int i = 0; i < R::NG; i++)
+                if ((i & 3) == t) *reinterpret_cast<unsigned *>(rec + R::kPK + (tok * R::NG + i) * 4) = params[i];
         }
     }
 #pragma unroll
     for (int half = 0; half < 2; half++) {
-        constexpr int N = D / 8;   // channels of a piece
-        constexpr int GP = G < N ? 1 : G / N;  // pieces a group
-        static_assert(G >= N, "a piece lies in one group");
-        const int row = u.tile * 8 + half * 4 + (lane >> 3), g = lane & 7;
-        int tok = 0;
-        bool mine;
-        const long long at = slot_of(p, row, u.head, layer + u.layer, tok, mine, status);
-        float x[N];
-        const uint16_t *src = v + u.layer * vls + row * vrs + (long long)u.head * D + g * N;
-#pragma unroll
-        for (int i = 0; i < N; i += 8) {
-            if (at >= 0) {
-                load8<BF, VEC>(src + i, x + i);
-            } else {
-#pragma unroll
-                for (int j = 0; j < 8; j++) x[i + j] = 0.0f;
-            }
-        }
-        float lo = x[0], hi = x[0];
-#pragma unroll
-        for (int i = 1; i < N; i++) widen(lo, hi, x[i], x[i]);
-#pragma unroll
-        for (int o = 1; o < GP; o <<= 1)
-            widen(lo, hi, __shfl_xor_sync(0xFFFFFFFFu, lo, o), __shfl_xor_sync(0xFFFFFFFFu, hi, o));
+        const int from = (half * 4 + (lane >> 3)) * 4;  // the lane that looked this row's slot up
+        const long long vat = __shfl_sync(0xFFFFFFFFu, at, from);
+        const int vtok = __shfl_sync(0xFFFFFFFFu, tok, from);
+        float lo, hi;
+        range_of<BF, N / 2>(z[half], 1, GP, lo, hi);
         const float s = group_scale<BF>(lo, hi);
+        unsigned words[N / 8];
+        codes_of<BF, N / 2>(z[half], lo, hi, s, words, [](int j) { return 2 * j; }, [](int j) { return 2 * j + 1; });
         if (s != s) {
-            bad |= at >= 0;
+            bad |= vat >= 0;
             lo = s;
         }
-        unsigned words[N / 8];
-#pragma unroll
-        for (int i = 0; i < N / 8; i++) {
-            words[i] = 0;
-#pragma unroll
-            for (int j = 0; j < 8; j++) words[i] |= code_of(x[8 * i + j], lo, s) << (4 * j);
-        }
-        if (at >= 0) {
-            uint8_t *rec = pool + at;
-            store_words<N / 8>(rec + R::kV + (tok >> 3) * (4 * D) + g * (D / 2) + (tok & 7) * (D / 16), words);
+        if (vat >= 0) {
+            uint8_t *rec = pool + vat;
+            store_words<N / 8>(rec + R::kV + (vtok >> 3) * (4 * D) + g * (D / 2) + (vtok & 7) * (D / 16), words);
             if (g % GP == 0)
-                *reinterpret_cast<unsigned *>(rec + R::kPV + (tok * R::NG + g / GP) * 4) =
+                *reinterpret_cast<unsigned *>(rec + R::kPV + (vtok * R::NG + g / GP) * 4) =
                     float_to_bits<BF>(s) | (float_to_bits<BF>(lo) << 16);
         }
     }
@@ -271,7 +302,9 @@ __device__ __forceinline__ void store_values(void *base, long long at, const flo
 }
 
 __device__ __forceinline__ float code_value(unsigned word, int nib, float s, float lo) {
-    return __fmaf_rn((float)((word >> (4 * nib)) & 15u), s, lo);  // the product is exact: one rounding
+    // 2^23 + c as bits, less 2^23: no conversion instruction; the product is exact, so one rounding
+    const float c = __uint_as_float(((word >> (4 * nib)) & 15u) | 0x4B000000u) - 8388608.0f;
+    return __fmaf_rn(c, s, lo);
 }
 
 template <int D, int G, int OUT, bool BF, bool VEC>
@@ -284,62 +317,62 @@ __global__ void __launch_bounds__(256) k_kv4_read(const uint8_t *__restrict__ po
     if (w >= (long long)tiles * p.H * nlayers) return;
     const int lane = threadIdx.x & 31;
     const Unit u = unit_of(p, w, tiles);
-    {
-        const int row = u.tile * 8 + (lane >> 2), t = lane & 3;
-        int tok = 0;
-        bool mine;
-        const long long at = slot_of(p, row, u.head, layer + u.layer, tok, mine, status);
-        unsigned words[W], params[R::NG];
+    const int row = u.tile * 8 + (lane >> 2), t = lane & 3, g = lane & 7;
+    int tok = 0;
+    bool mine;
+    const long long at = slot_of(p, row, u.head, layer + u.layer, tok, mine, status);
+    constexpr int N = D / 8;
+    unsigned words[W], params[R::NG], vw[2][N / 8], vp[2];
 #pragma unroll
-        for (int i = 0; i < W; i++) words[i] = 0;
+    for (int i = 0; i < W; i++) words[i] = 0;
 #pragma unroll
-        for (int g = 0; g < R::NG; g++) params[g] = 0;
-        if (at >= 0) {
-            const uint8_t *rec = pool + at;
-            load_words<W>(rec + (tok >> 3) * (4 * D) + (tok & 7) * (D / 2) + t * (D / 8), words);
+    for (int i = 0; i < R::NG; i++) params[i] = 0;
+    if (at >= 0) {
+        const uint8_t *rec = pool + at;
+        load_words<W>(rec + (tok >> 3) * (4 * D) + (tok & 7) * (D / 2) + t * (D / 8), words);
 #pragma unroll
-            for (int g = 0; g < R::NG; g++)
-                params[g] = *reinterpret_cast<const unsigned *>(rec + R::kPK + (tok * R::NG + g) * 4);
+        for (int i = 0; i < R::NG; i++)
+            params[i] = *reinterpret_cast<const unsigned *>(rec + R::kPK + (tok * R::NG + i) * 4);
+    }
+    bool vmine[2];
+#pragma unroll
+    for (int half = 0; half < 2; half++) {
+        const int from = (half * 4 + (lane >> 3)) * 4;  // the lane that looked this row's slot up
+        const long long vat = __shfl_sync(0xFFFFFFFFu, at, from);
+        const int vtok = __shfl_sync(0xFFFFFFFFu, tok, from);
+        vmine[half] = __shfl_sync(0xFFFFFFFFu, (int)mine, from);
+        vp[half] = 0;
+#pragma unroll
+        for (int i = 0; i < N / 8; i++) vw[half][i] = 0;
+        if (vat >= 0) {
+            const uint8_t *rec = pool + vat;
+            load_words<N / 8>(rec + R::kV + (vtok >> 3) * (4 * D) + g * (D / 2) + (vtok & 7) * (D / 16), vw[half]);
+            vp[half] = *reinterpret_cast<const unsigned *>(rec + R::kPV + (vtok * R::NG + g * N / G) * 4);
         }
-        if (mine) {
-            const long long dst = u.layer * ls + row * rs + (long long)u.head * D + 4 * t;
+    }
+    if (mine) {
+        const long long dst = u.layer * ls + row * rs + (long long)u.head * D + 4 * t;
 #pragma unroll
-            for (int j = 0; j < D / 16; j++) {
-                const unsigned pr = params[16 * j / G];
-                const float s = bits_to_float<BF>(pr & 0xFFFFu), lo = bits_to_float<BF>(pr >> 16);
-                float x[4];
+        for (int j = 0; j < D / 16; j++) {
+            const unsigned pr = params[16 * j / G];
+            const float s = bits_to_float<BF>(pr & 0xFFFFu), lo = bits_to_float<BF>(pr >> 16);
+            float x[4];
 #pragma unroll
-                for (int e = 0; e < 4; e++)
-                    x[e] = code_value(words[j >> 1], 4 * (e & 1) + 2 * (j & 1) + (e >> 1), s, lo);
-                store_values<OUT, VEC, 4>(ok, dst + 16 * j, x);
-            }
+            for (int e = 0; e < 4; e++) x[e] = code_value(words[j >> 1], 4 * (e & 1) + 2 * (j & 1) + (e >> 1), s, lo);
+            store_values<OUT, VEC, 4>(ok, dst + 16 * j, x);
         }
     }
 #pragma unroll
     for (int half = 0; half < 2; half++) {
-        constexpr int N = D / 8;
-        const int row = u.tile * 8 + half * 4 + (lane >> 3), g = lane & 7;
-        int tok = 0;
-        bool mine;
-        const long long at = slot_of(p, row, u.head, layer + u.layer, tok, mine, status);
-        unsigned words[N / 8], pr = 0;
+        if (!vmine[half]) continue;
+        const float s = bits_to_float<BF>(vp[half] & 0xFFFFu), lo = bits_to_float<BF>(vp[half] >> 16);
+        const long long dst = u.layer * ls + (u.tile * 8 + half * 4 + (lane >> 3)) * rs + (long long)u.head * D + g * N;
 #pragma unroll
-        for (int i = 0; i < N / 8; i++) words[i] = 0;
-        if (at >= 0) {
-            const uint8_t *rec = pool + at;
-            load_words<N / 8>(rec + R::kV + (tok >> 3) * (4 * D) + g * (D / 2) + (tok & 7) * (D / 16), words);
-            pr = *reinterpret_cast<const unsigned *>(rec + R::kPV + (tok * R::NG + g * N / G) * 4);
-        }
-        if (mine) {
-            const float s = bits_to_float<BF>(pr & 0xFFFFu), lo = bits_to_float<BF>(pr >> 16);
-            const long long dst = u.layer * ls + row * rs + (long long)u.head * D + g * N;
+        for (int i = 0; i < N; i += 8) {
+            float x[8];
 #pragma unroll
-            for (int i = 0; i < N; i += 8) {
-                float x[8];
-#pragma unroll
-                for (int j = 0; j < 8; j++) x[j] = code_value(words[i / 8], j, s, lo);
-                store_values<OUT, VEC, 8>(ov, dst + i, x);
-            }
+            for (int j = 0; j < 8; j++) x[j] = code_value(vw[half][i / 8], j, s, lo);
+            store_values<OUT, VEC, 8>(ov, dst + i, x);
         }
     }
 }
