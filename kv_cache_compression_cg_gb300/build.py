@@ -17,7 +17,8 @@ CSRC = os.path.join(HERE, "csrc")
 BUILD_DIR = os.path.join(HERE, "_build")
 LIB_PATH = os.path.join(HERE, "libcachegen_gb300.so")
 SOURCES = ["quant.cu", "codec.cu", "compress.cu", "decode.cu", "decode_delta.cu", "scan.cu", "records3.cu",
-           "capi.cu", "noalloc.cu", "kv4_capi.cu", "kv4_store.cu", "kv4_step.cu"]
+           "capi.cu", "noalloc.cu", "kv4_capi.cu", "kv4_store.cu", "kv4_step.cu",
+           "kv4_chunk.cu"]
 HEADERS = [os.path.join(CSRC, "cg_internal.cuh"), os.path.join(CSRC, "coder.cuh"),
            os.path.join(CSRC, "decode_pipe.cuh"), os.path.join(CSRC, "kv4.cuh"),
            os.path.join(ROOT, "include", "cachegen.h")]

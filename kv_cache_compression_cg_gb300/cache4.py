@@ -72,6 +72,7 @@ class Batch4:
         self._c = capi.cg_kv4_batch(B, table.shape[1], self.rows, self.max_rows, table.data_ptr(), kv_len.data_ptr(),
                                     None if start is None else start.data_ptr())
         self._ref = C.byref(self._c)
+        self._need: dict[tuple, int] = {}  # workspace bytes by the cache's shape and the query heads
 
 
 class Cache4:
@@ -107,23 +108,26 @@ class Cache4:
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self._pool, self._status, self._device = pool.data_ptr(), self.status.data_ptr(), pool.get_device()
         self._at = pool.device
-        one = capi.cg_kv4_batch()
-        self._ws_bytes = int(self._lib.cg_kv4_attention_workspace_bytes(self._ref, C.byref(one), H))
         self._ws: dict[int, torch.Tensor] = {}  # attention's workspace of each stream
         # arguments that every call repeats, as the binding takes them
         self._a = (C.c_void_p(self._pool), self._ref)
+        self._shape = (H, D, group)
         self._fn = {n: getattr(self._lib, "cg_kv4_" + n) for n in ("write", "read", "attention")}
         self._scale = D ** -0.5
 
     def _stream(self, stream) -> int:
         return _current(self._device) if stream is None else stream.cuda_stream
 
-    def _workspace(self, stream: int) -> torch.Tensor:
+    def _workspace(self, stream: int, batch: Batch4, Hq: int) -> torch.Tensor:
         """The stream's workspace. Calls on one stream follow one another and may
         share it; a captured call, which may be replayed on any, gets its own."""
+        need = batch._need.get((self._shape, Hq))
+        if need is None:
+            need = int(self._lib.cg_kv4_attention_workspace_bytes(self._ref, batch._ref, Hq))
+            batch._need[self._shape, Hq] = need
         ws = self._ws.get(stream)
-        if ws is None or _capturing():
-            ws = torch.zeros(self._ws_bytes, dtype=torch.uint8, device=self._at)
+        if ws is None or ws.numel() < need or _capturing():
+            ws = torch.zeros(need, dtype=torch.uint8, device=self._at)
             if not _capturing():
                 self._ws[stream] = ws
         return ws
@@ -239,10 +243,10 @@ class Cache4:
             out_stride = out.stride(0)
         lse = torch.empty((batch.rows, Hq), dtype=torch.float32, device=self._at) if return_lse else None
         stream = _current(self._device)
-        ws = self._workspace(stream)
+        ws = self._workspace(stream, batch, Hq)
         code = self._fn["attention"](
             *self._a, batch._ref, layer, Hq, q.data_ptr(), q_stride, self._scale if scale is None else scale, window,
-            out.data_ptr(), out_stride, None if lse is None else lse.data_ptr(), ws.data_ptr(), self._ws_bytes,
+            out.data_ptr(), out_stride, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
             self._status, stream)
         if code:
             capi.check(code, "cg_kv4_attention")

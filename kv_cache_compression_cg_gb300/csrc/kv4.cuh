@@ -135,11 +135,16 @@ struct Kv4Attend {
     void *ws;                 // tickets (ticket_bytes, zero between calls), then partial results
     long long ticket_bytes;
     bool q_vec, out_vec;      // rows allow 8-byte loads, stores
+    bool out_vec16;           // and 16-byte stores
+    int step_max;             // (rows x R) of a sequence up to which it is the step kernel's,
+    int chunk_min;            // from which on the chunk kernel's
 };
 
 uint64_t kv4_ticket_bytes();
 uint64_t kv4_step_workspace_bytes(const Kv4 &p);
 
+uint64_t kv4_chunk_workspace_bytes(const Kv4 &p);
+cudaError_t launch_kv4_chunk(const Kv4 &p, const Kv4Attend &a, cudaStream_t s);
 cudaError_t launch_kv4_step(const Kv4 &p, const Kv4Attend &a, cudaStream_t s);
 
 }  // namespace cg

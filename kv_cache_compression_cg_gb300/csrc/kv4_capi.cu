@@ -64,6 +64,21 @@ bool strides_ok(const cg_kv4_shape *s, const cg_kv4_batch *b, int32_t n, int64_t
     return row >= 0;
 }
 
+// Which kernels a call of attention takes. A sequence of up to kStepCols (row, query head of a KV head)
+// pairs is the step kernel's, more are the chunk kernel's. With one of each kind both run, on
+// their own sequences; where the average is past the limit the chunk kernel takes them all, which saves the
+// other launch.
+constexpr int kStepCols = 64;
+struct Plan {
+    bool step, chunk;
+};
+Plan plan_of(const Kv4 &p, int R) {
+    Plan plan;
+    plan.chunk = p.D < 256 && (long long)p.max_rows * R > kStepCols;
+    plan.step = !plan.chunk || (long long)p.rows * R <= (long long)p.B * kStepCols;
+    return plan;
+}
+
 cg_status launched(cudaError_t e) { return e == cudaSuccess ? CG_OK : CG_ERR_CUDA; }
 
 }  // namespace
@@ -116,7 +131,10 @@ uint64_t cg_kv4_attention_workspace_bytes(const cg_kv4_shape *shape, const cg_kv
     if (!shape_ok(shape) || !batch_ok(batch) || Hq < 1 || Hq % shape->H) return 0;
     Kv4 p;
     prepare(shape, batch, p);
-    return (cg::kv4_step_workspace_bytes(p) + 255) / 256 * 256;
+    const Plan plan = plan_of(p, Hq / shape->H);
+    uint64_t n = plan.step ? cg::kv4_step_workspace_bytes(p) : 0;
+    if (plan.chunk && cg::kv4_chunk_workspace_bytes(p) > n) n = cg::kv4_chunk_workspace_bytes(p);
+    return (n + 255) / 256 * 256;
 }
 
 cg_status cg_kv4_attention(const uint8_t *pool, const cg_kv4_shape *shape, const cg_kv4_batch *batch, int32_t layer,
@@ -152,7 +170,15 @@ cg_status cg_kv4_attention(const uint8_t *pool, const cg_kv4_shape *shape, const
     a.ticket_bytes = (long long)cg::kv4_ticket_bytes();
     a.q_vec = aligned(q, 8) && q_row_stride % 4 == 0;
     a.out_vec = aligned(out, 8) && out_row_stride % 4 == 0;
-    return launched(cg::launch_kv4_step(p, a, stream));
+    a.out_vec16 = aligned(out, 16) && out_row_stride % 8 == 0;
+    const Plan plan = plan_of(p, a.R);
+    a.step_max = plan.chunk ? kStepCols : 0x7FFFFFFF;
+    a.chunk_min = plan.step ? kStepCols + 1 : 0;
+    if (plan.step) {
+        const cudaError_t e = cg::launch_kv4_step(p, a, stream);
+        if (e != cudaSuccess || !plan.chunk) return launched(e);
+    }
+    return launched(cg::launch_kv4_chunk(p, a, stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,921 @@
+// kv4_chunk.cu - attention of many query rows over the 4-bit paged cache (N in
+// include/cachegen.h): prompts and their chunks, on tcgen05.
+//
+// A work item is 256 rows (two tiles of 128; a row is a (row of the batch, query head) pair that shares the KV
+// head) against the key tiles of 128 tokens that they see. Warps of a CTA:
+//   0-3, 4-7   softmax of either row tile: a thread owns a row, that is a lane of tensor memory
+//   8-11       K and V: codes and parameters from the pool to registers (a tile ahead), to binary16 in
+//              shared memory, two stages
+//   12         issues the matrix instructions
+// While one tile's softmax runs the tensor cores work for the other one:
+//   ... P0 V, Q0 K', P1 V, Q1 K', ...
+// Rounding. K goes in as s c, exact in binary16 (seven bits times four) under a power of two of the tile; the
+// minima enter as 16 more channels: m_g against the sum of the row's q over the group, that sum as
+// a high and a low part. So scores are exact up to binary32 sums. V goes in as c s + m with one rounding
+// under a power of two that follows the largest |V^|; weights are rounded to binary16, sums are binary32.
+// A row's maximum is only raised once the scores pass it by 8 (base 2): accumulators are rarely rescaled.
+//
+// The units of all items (row tile pair x key tile) are dealt out in equal contiguous ranges to one CTA an
+// SM; CTAs that share an item leave partial results, which the last of them joins in order.
+#include "kv4.cuh"
+
+namespace cg {
+namespace {
+
+constexpr int kKT = 128;          // keys a tile
+constexpr int kRows = 256;        // rows an item
+constexpr int kThreads = 13 * 32;
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr float kMaxF = 3.402823466e38f;
+constexpr int kSigMin = -110;
+constexpr unsigned kWaitLimit = 1u << 20;  // polls of one wait (each up to some microseconds): far above any real one
+
+// ---- PTX -------------------------------------------------------------------
+__device__ __forceinline__ unsigned saddr(const void *p) { return (unsigned)__cvta_generic_to_shared(p); }
+__device__ __forceinline__ void bar_init(unsigned bar, unsigned count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(bar), "r"(count) : "memory");
+}
+__device__ __forceinline__ void bar_arrive(unsigned bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void mma_ss(unsigned d, uint64_t a, uint64_t b, unsigned idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((unsigned)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(unsigned d, unsigned a, uint64_t b, unsigned idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((unsigned)add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_commit(unsigned bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+#define CG_R8(f, o) f[o], f[o + 1], f[o + 2], f[o + 3], f[o + 4], f[o + 5], f[o + 6], f[o + 7]
+__device__ __forceinline__ void tmem_ld32(unsigned addr, unsigned *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(addr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st32(unsigned addr, const unsigned *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
+        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(unsigned addr, const unsigned *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(addr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Shared memory matrix: rows (K-major) or tokens (MN-major) of 128 bytes in blocks of 8, swizzled by 128 bytes;
+// lead: bytes between 64-channel blocks along the contiguous side of an MN-major matrix.
+__device__ __forceinline__ uint64_t desc128(unsigned addr, unsigned lead) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
+           (1ull << 46) | (2ull << 61);
+}
+// 16 channels a row, without swizzle: blocks of 8 rows x 16 bytes, 128 bytes each; the two blocks of 8 channels
+// are 128 bytes apart, blocks of 8 rows 256.
+__device__ __forceinline__ uint64_t desc_narrow(unsigned addr) {
+    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(256 >> 4) << 32) |
+           (1ull << 46);
+}
+// kind::f16, binary16 in, binary32 out, M = 128.
+__host__ __device__ constexpr unsigned idesc_f16(int n, bool b_mn) {
+    return (1u << 4) | ((unsigned)b_mn << 16) | ((unsigned)(n >> 3) << 17) | (8u << 24);
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+__device__ __forceinline__ unsigned pack_half(float lo, float hi) {
+    unsigned y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+__device__ __forceinline__ unsigned fma_half(unsigned a, unsigned b, unsigned c) {
+    unsigned y;
+    asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+    return y;
+}
+__device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
+
+// ---- shared memory ----------------------------------------------------------
+template <int D>
+struct Smem {
+    static constexpr int kQ = 0;                         // [tile][D/64][128 rows x 128 bytes]
+    static constexpr int kQTile = 128 * D * 2;
+    static constexpr int kK = 2 * kQTile;                // [stage][D/64][128 x 128]
+    static constexpr int kKStage = kKT * D * 2;
+    static constexpr int kV = kK + 2 * kKStage;          // [stage][D/64][128 tokens x 128]
+    static constexpr int kQN = kV + 2 * kKStage;         // narrow: [tile][128 x 16]
+    static constexpr int kKN = kQN + 2 * 4096;           // [stage][128 x 16]
+    static constexpr int kBytes = kKN + 2 * 4096 + 1024; // and the alignment of the first
+};
+
+struct Info {
+    int ek, ev;       // powers of two of the tile's K and V
+    unsigned valid;   // records that have a page
+    unsigned odd;     // some value group is not finite
+};
+
+struct Segment {
+    int b, kvh, row0, first, n, len, t0, tiles, ua, ub, whole;
+    long long pos0;
+    long long item_u0, item_u1;
+    int more;
+};
+
+// The sequence's rows for this kernel, and per row tile pair its key tiles.
+struct Span {
+    int first, n, len;
+    long long pos0;
+};
+__device__ __forceinline__ Span span_of(const Kv4 &p, const Kv4Attend &a, int b, int32_t *status) {
+    Span s;
+    seq_rows(p, b, s.first, s.n, status);
+    if ((long long)s.n * a.R < a.chunk_min) s.n = 0;
+    s.len = s.n ? seq_len(p, b, status) : 0;
+    s.pos0 = (long long)p.kv_len[b] - s.n;
+    return s;
+}
+__device__ __forceinline__ void tiles_of(const Span &s, const Kv4Attend &a, int pair, int &t0, int &tiles) {
+    const int last_row = min((pair + 1) * kRows, s.n * a.R) - 1;
+    const long long hi = s.pos0 + last_row / a.R, lo = s.pos0 + (long long)pair * kRows / a.R;
+    const long long end = hi < s.len ? hi + 1 : s.len;  // keys before it are seen by some row
+    const long long begin = a.window && lo + 1 > a.window ? lo + 1 - a.window : 0;
+    t0 = 0;
+    tiles = 1;  // a pair without keys still has outputs
+    if (end > begin) {
+        t0 = (int)(begin / kKT);
+        tiles = (int)((end + kKT - 1) / kKT) - t0;
+    }
+}
+__device__ __forceinline__ long long units_of(const Kv4 &p, const Kv4Attend &a, int b, int32_t *status) {
+    const Span s = span_of(p, a, b, status);
+    const int pairs = (s.n * a.R + kRows - 1) / kRows;
+    long long sum = 0;
+    for (int i = 0; i < pairs; i++) {
+        int t0, tiles;
+        tiles_of(s, a, i, t0, tiles);
+        sum += tiles;
+    }
+    return sum * p.H;
+}
+__device__ __forceinline__ long long cta_of(long long u, long long total, long long grid) {
+    long long c = u * grid / total;
+    while (total * c / grid > u) c--;
+    while (total * (c + 1) / grid <= u) c++;
+    return c;
+}
+
+// Partial result of a CTA: [D / 4][256 rows] of 4 accumulators, then maximum, sum and bits of each row.
+template <int D>
+__host__ __device__ constexpr long long partial_floats() { return (long long)kRows * D + 3 * kRows; }
+
+template <int D, int G, bool BF>
+__global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant__ Kv4 p, const __grid_constant__ Kv4Attend a) {
+    using R = Rec<D, G>;
+    using S = Smem<D>;
+    constexpr int NG = R::NG, W = D / 32, NB = D / 64;
+    constexpr int kS0 = 0, kO0 = 256;  // columns of tensor memory: S of either tile 128, O of either D
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) uint64_t bars[16];
+    __shared__ unsigned s_tmem, s_stop, s_last;
+    __shared__ Info s_info[4];
+    __shared__ uint8_t s_odd[4][kKT];  // bits of a token's value groups that are not finite
+    __shared__ float s_emax[2][2][4];
+    __shared__ Segment s_seg;
+    __shared__ long long s_sum[13];
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    uint8_t *sm = raw + ((1024 - (saddr(raw) & 1023)) & 1023);
+    const unsigned smb = saddr(sm);
+    const unsigned bb = saddr(bars);
+    const unsigned k_full = bb, k_empty = bb + 16, v_full = bb + 32, v_empty = bb + 48, s_full = bb + 64, p_full = bb + 80,
+                   o_done = bb + 96;  // two of each
+
+    // ---- how much work there is, and where this CTA's range begins
+    long long sum = 0;
+    for (int b = threadIdx.x; b < p.B; b += kThreads) sum += units_of(p, a, b, a.status);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+    if (lane == 0) s_sum[warp] = sum;
+    if (threadIdx.x == 0) {
+        s_stop = 0;
+        for (int i = 0; i < 2; i++) {
+            bar_init(k_full + 8 * i, 128);
+            bar_init(k_empty + 8 * i, 1);
+            bar_init(v_full + 8 * i, 128);
+            bar_init(v_empty + 8 * i, 1);
+            bar_init(s_full + 8 * i, 1);
+            bar_init(p_full + 8 * i, 128);
+            bar_init(o_done + 8 * i, 1);
+        }
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    long long total = 0;
+    for (int i = 0; i < 13; i++) total += s_sum[i];
+    const long long grid = total < gridDim.x ? total : gridDim.x;
+    if (blockIdx.x >= grid) return;
+    long long u = total * blockIdx.x / grid;
+    const long long u_end = total * (blockIdx.x + 1) / grid;
+
+    if (warp == 12) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(&s_tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        fence_before();
+    }
+    // the sequence that unit u belongs to; kept by warp 0
+    int cur_b = 0;
+    long long before = 0;
+    if (warp == 0) {
+        for (int b0 = 0; b0 < p.B; b0 += 32) {
+            const long long x = b0 + lane < p.B ? units_of(p, a, b0 + lane, nullptr) : 0;
+            long long incl = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if (lane >= o) incl += y;
+            }
+            const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + incl > u);
+            if (hit) {
+                const int src = __ffs(hit) - 1;
+                cur_b = b0 + src;
+                before += __shfl_sync(0xFFFFFFFFu, incl - x, src);
+                break;
+            }
+            before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+        }
+    }
+    __syncthreads();
+    fence_after();
+    const unsigned tmem = s_tmem;
+
+    // Waits are bounded: the first to run out stops all others, and the call reports CG_FLAG_TIMEOUT.
+    auto wait = [&](unsigned bar, unsigned parity) {
+        for (unsigned i = 0; !bar_try(bar, parity); i++) {
+            if (*(volatile unsigned *)&s_stop) return;
+            if (i >= kWaitLimit) {
+                *(volatile unsigned *)&s_stop = 1;
+                raise_flag(a.status, CG_FLAG_TIMEOUT);
+                return;
+            }
+        }
+    };
+
+    unsigned *tickets = static_cast<unsigned *>(a.ws);
+    float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + a.ticket_bytes);
+    unsigned n_kv = 0;       // key tiles this CTA has begun: stage and parity of K, V
+    unsigned n_q[2] = {0, 0};  // tiles of S, P, O of either row tile
+
+    while (u < u_end) {
+        // ---- the item of unit u
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            Segment g;
+            long long all = units_of(p, a, cur_b, nullptr);
+            while (u - before >= all) {
+                before += all;
+                cur_b++;
+                all = units_of(p, a, cur_b, nullptr);
+            }
+            const Span s = span_of(p, a, cur_b, nullptr);
+            const long long per = all / p.H;
+            long long rest = (u - before) % per;
+            g.b = cur_b;
+            g.kvh = (int)((u - before) / per);
+            int pair = 0;
+            tiles_of(s, a, 0, g.t0, g.tiles);
+            while (rest >= g.tiles) {
+                rest -= g.tiles;
+                tiles_of(s, a, ++pair, g.t0, g.tiles);
+            }
+            g.row0 = pair * kRows;
+            g.first = s.first;
+            g.n = s.n;
+            g.len = s.len;
+            g.pos0 = s.pos0;
+            g.ua = (int)rest;
+            g.ub = u_end - u < g.tiles - rest ? (int)(rest + u_end - u) : g.tiles;
+            g.whole = g.ua == 0 && g.ub == g.tiles;
+            g.item_u0 = u - rest;
+            g.item_u1 = g.item_u0 + g.tiles;
+            s_seg = g;
+        }
+        __syncthreads();
+        const Segment g = s_seg;
+        const int n_rows = g.n * a.R - g.row0;               // of this pair; may pass 256
+        const int nq = n_rows > 128 ? 2 : 1;
+        const int tile0 = g.t0 + g.ua, n_tiles = g.ub - g.ua;
+
+        // ---- queries: row r of the pair, under 2^kq of its own; a chunk of 16 bytes holds channels 32w + 4t + 0..3 and
+        // 16 more on, w = 2 block + chunk % 2, t = chunk / 2: the order K's chunks come in
+        const int q = warp >> 2;                               // softmax warps: their tile
+        const int r = threadIdx.x & 127, rho = g.row0 + q * 128 + r;
+        const bool mine = warp < 8 && rho < g.n * a.R;
+        const int irow = rho / a.R, head = g.kvh * a.R + rho % a.R;
+        float factor = 0.0f;
+        if (warp < 8) {
+            const uint16_t *src = a.q + (long long)(g.first + irow) * a.q_stride + (long long)head * D;
+            auto four = [&](int d, unsigned &x, unsigned &y) {
+                x = y = 0;
+                if (!mine) return;
+                if (a.q_vec) {
+                    const uint2 w = *reinterpret_cast<const uint2 *>(src + d);
+                    x = w.x;
+                    y = w.y;
+                } else {
+                    x = src[d] | ((unsigned)src[d + 1] << 16);
+                    y = src[d + 2] | ((unsigned)src[d + 3] << 16);
+                }
+            };
+            float top = 0.0f;
+#pragma unroll 8
+            for (int d = 0; d < D; d += 4) {
+                unsigned x, y;
+                four(d, x, y);
+                top = fmaxf(top, fmaxf(fmaxf(fabsf(bits_to_float<BF>(x & 0xFFFFu)), fabsf(bits_to_float<BF>(x >> 16))),
+                                       fmaxf(fabsf(bits_to_float<BF>(y & 0xFFFFu)), fabsf(bits_to_float<BF>(y >> 16)))));
+            }
+            // the row's largest goes to [2^7, 2^8): sums over a group stay below 2^15
+            int kq = top > 0.0f ? 7 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
+            kq = kq > 120 ? 120 : kq;
+            const float f = a.scale < 0.0f ? -pow2f(kq) : pow2f(kq);
+            factor = fabsf(a.scale) * kLog2e * pow2f(-kq);
+            uint8_t *dst = sm + S::kQ + q * S::kQTile + r * 128;
+            float sums[NG];
+#pragma unroll
+            for (int i = 0; i < NG; i++) sums[i] = 0.0f;
+#pragma unroll
+            for (int c = 0; c < D / 8; c++) {
+                const int block = c / 8, chunk = c % 8, w = 2 * block + (chunk & 1), t = chunk >> 1;
+                unsigned x[4];
+                four(32 * w + 4 * t, x[0], x[1]);
+                four(32 * w + 16 + 4 * t, x[2], x[3]);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    x[i] = pack_half(bits_to_float<BF>(x[i] & 0xFFFFu) * f, bits_to_float<BF>(x[i] >> 16) * f);
+                    const float2 y = __half22float2(*reinterpret_cast<__half2 *>(&x[i]));
+                    sums[32 * w / G] += y.x + y.y;
+                }
+                *reinterpret_cast<uint4 *>(dst + block * 16384 + ((chunk ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+            }
+            // channels 0.. of the narrow block: high parts of the sums, then low parts
+            float nar[16];
+#pragma unroll
+            for (int i = 0; i < 16; i++) nar[i] = 0.0f;
+#pragma unroll
+            for (int i = 0; i < NG; i++) {
+                const float hi = __half2float(__float2half_rn(sums[i]));
+                nar[i] = hi;
+                nar[NG + i] = sums[i] - hi;
+            }
+            uint8_t *nd = sm + S::kQN + q * 4096 + (r >> 3) * 256 + (r & 7) * 16;
+#pragma unroll
+            for (int h = 0; h < 2; h++)
+                *reinterpret_cast<uint4 *>(nd + h * 128) =
+                    make_uint4(pack_half(nar[8 * h], nar[8 * h + 1]), pack_half(nar[8 * h + 2], nar[8 * h + 3]),
+                               pack_half(nar[8 * h + 4], nar[8 * h + 5]), pack_half(nar[8 * h + 6], nar[8 * h + 7]));
+            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+        }
+        __syncthreads();
+
+        if (warp == 12) {
+            // ---- matrix instructions
+            if (lane == 0) {
+                constexpr unsigned id_s = idesc_f16(kKT, false), id_o = idesc_f16(D, true);
+                auto scores = [&](int i, unsigned kv) {
+                    const unsigned st = kv & 1, d = tmem + kS0 + i * kKT;
+#pragma unroll
+                    for (int k = 0; k < D / 16; k++) {
+                        const unsigned off = (k / 4) * 16384 + (k % 4) * 32;
+                        mma_ss(d, desc128(smb + S::kQ + i * S::kQTile + off, 16), desc128(smb + S::kK + st * S::kKStage + off, 16),
+                               id_s, k > 0);
+                    }
+                    mma_ss(d, desc_narrow(smb + S::kQN + i * 4096), desc_narrow(smb + S::kKN + st * 4096), id_s, true);
+                    mma_commit(s_full + 8 * i);
+                };
+                unsigned kv = n_kv;
+                wait(k_full + 8 * (kv & 1), (kv >> 1) & 1);
+                fence_after();
+                for (int i = 0; i < nq; i++) scores(i, kv);
+                mma_commit(k_empty + 8 * (kv & 1));
+                for (int j = 0; j < n_tiles; j++, kv++) {
+                    wait(v_full + 8 * (kv & 1), (kv >> 1) & 1);
+                    for (int i = 0; i < nq; i++) {
+                        wait(p_full + 8 * i, (n_q[i] + j) & 1);
+                        fence_after();
+                        const unsigned st = kv & 1, d = tmem + kO0 + i * D, pa = tmem + kS0 + i * kKT;
+#pragma unroll
+                        for (int k = 0; k < kKT / 16; k++)
+                            mma_ts(d, pa + 8 * k, desc128(smb + S::kV + st * S::kKStage + k * 2048, 16384), id_o, j > 0 || k > 0);
+                        mma_commit(o_done + 8 * i);
+                        if (i == nq - 1) mma_commit(v_empty + 8 * st);
+                        if (j + 1 < n_tiles) {
+                            if (i == 0) {
+                                wait(k_full + 8 * ((kv + 1) & 1), ((kv + 1) >> 1) & 1);
+                                fence_after();
+                            }
+                            scores(i, kv + 1);
+                            if (i == nq - 1) mma_commit(k_empty + 8 * ((kv + 1) & 1));
+                        }
+                    }
+                }
+            }
+            __syncwarp();
+        } else if (warp >= 8) {
+            // ---- K and V of a tile: warp w has records 2w, 2w + 1; lanes as in the step kernel
+            const int w = warp - 8, gl = lane >> 2, t = lane & 3, gv = gl * (D / 8) / G;
+            const int *table = p.table + (long long)g.b * p.max_pages;
+            const int rpp = p.P / kBlk;
+            auto page_at = [&](int j) {  // lanes 0, 1: pages of the warp's records of tile j
+                int pg = -1;
+                const long long tok = (long long)(tile0 + j) * kKT + (2 * w + (lane & 1)) * kBlk;
+                if (j < n_tiles && lane < 2 && tok < g.len) {
+                    pg = table[(int)(tok / p.P)];
+                    if (pg < 0 || pg >= p.pages) {
+                        raise_flag(a.status, CG_FLAG_BATCH);
+                        pg = -1;
+                    }
+                }
+                return pg;
+            };
+            unsigned kr[2][2][W], vr[2][2][W], kp[2][2][NG], vp[2][2][2];
+            unsigned ok = 0;
+            auto fetch = [&](int j, int pg) {
+                ok = 0;
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const int page = __shfl_sync(0xFFFFFFFFu, pg, i);
+                    const int rec = (tile0 + j) * (kKT / kBlk) + 2 * w + i;
+                    if (page >= 0) {
+                        ok |= 1u << i;
+                        const uint8_t *src = a.pool + page * p.page_stride + ((long long)g.kvh * rpp + rec % rpp) * R::kBytes;
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+                            const uint8_t *kc = src + h * 4 * D + lane * (D / 8), *vc = src + R::kV + h * 4 * D + lane * (D / 8);
+                            if (W == 2) {
+                                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(kc)), y = __ldg(reinterpret_cast<const uint2 *>(vc));
+                                kr[i][h][0] = x.x, kr[i][h][1] = x.y, vr[i][h][0] = y.x, vr[i][h][1] = y.y;
+                            } else {
+#pragma unroll
+                                for (int c = 0; c + 3 < W; c += 4) {
+                                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(kc) + c / 4);
+                                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(vc) + c / 4);
+                                    kr[i][h][c] = x.x, kr[i][h][c + 1] = x.y, kr[i][h][c + 2] = x.z, kr[i][h][c + 3] = x.w;
+                                    vr[i][h][c] = y.x, vr[i][h][c + 1] = y.y, vr[i][h][c + 2] = y.z, vr[i][h][c + 3] = y.w;
+                                }
+                            }
+                            const unsigned *pk = reinterpret_cast<const unsigned *>(src + R::kPK) + (8 * h + gl) * NG;
+#pragma unroll
+                            for (int c = 0; c < NG; c++) kp[i][h][c] = __ldg(pk + c);
+                            const unsigned *pv = reinterpret_cast<const unsigned *>(src + R::kPV) + (8 * h + 2 * t) * NG + gv;
+                            vp[i][h][0] = __ldg(pv);
+                            vp[i][h][1] = __ldg(pv + NG);
+                        }
+                    } else {
+#pragma unroll
+                        for (int h = 0; h < 2; h++) {
+#pragma unroll
+                            for (int c = 0; c < W; c++) kr[i][h][c] = vr[i][h][c] = 0;
+#pragma unroll
+                            for (int c = 0; c < NG; c++) kp[i][h][c] = 0;
+                            vp[i][h][0] = vp[i][h][1] = 0;
+                        }
+                    }
+                }
+            };
+            fetch(0, page_at(0));
+            int pg_next = page_at(1);
+            int sig = kSigMin;
+            for (int j = 0; j < n_tiles; j++) {
+                const unsigned kv = n_kv + j, st = kv & 1, par = ((kv >> 1) & 1) ^ 1;
+                const int base = (tile0 + j) * kKT + 2 * w * kBlk;
+                // parameters of tokens that the sequence does not hold count as zero; a value group that is not finite too
+                // (its rows are found by their bits), a key group's NaN stays
+                float kmax = 0.0f, vmax = 0.0f;
+                unsigned odd = 0;
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        if (base + i * kBlk + 8 * h + gl >= g.len)
+#pragma unroll
+                            for (int c = 0; c < NG; c++) kp[i][h][c] = 0;
+#pragma unroll
+                        for (int c = 0; c < NG; c++)
+                            kmax = fmaxf(kmax, fmaxf(15.0f * bits_to_float<BF>(kp[i][h][c] & 0xFFFFu), fabsf(bits_to_float<BF>(kp[i][h][c] >> 16))));
+#pragma unroll
+                        for (int y = 0; y < 2; y++) {
+                            const float s = bits_to_float<BF>(vp[i][h][y] & 0xFFFFu), m = bits_to_float<BF>(vp[i][h][y] >> 16);
+                            const bool held = base + i * kBlk + 8 * h + 2 * t + y < g.len, fine = fabsf(s) <= kMaxF && fabsf(m) <= kMaxF;
+                            if (held && !fine) odd |= 1u << (4 * i + 2 * h + y);
+                            if (!held || !fine) vp[i][h][y] = 0;
+                            else vmax = fmaxf(vmax, fmaxf(fabsf(m), fabsf(fmaf(15.0f, s, m))));
+                        }
+                    }
+                const unsigned ku = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(kmax, kMaxF)));
+                const unsigned vu = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(vmax, kMaxF)));
+                if (lane == 0) {
+                    s_emax[j & 1][0][w] = __uint_as_float(ku);
+                    s_emax[j & 1][1][w] = __uint_as_float(vu);
+                }
+                const unsigned any_odd = __ballot_sync(0xFFFFFFFFu, odd != 0);
+                Info *info = &s_info[kv & 3];
+                // the entry's last readers are done: this tile's K stage is free only after the scores two tiles on
+                wait(k_empty + 8 * st, par);
+                if (w == 0 && lane == 0) {
+                    info->valid = 0;
+                    info->odd = 0;
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                if (lane == 0) {
+                    atomicOr(&info->valid, ok << (2 * w));
+                    if (any_odd) atomicOr(&info->odd, 1u << w);
+                }
+                if (any_odd) {  // rare: bits of each token's groups
+                    s_odd[kv & 3][2 * w * kBlk + lane] = 0;
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 2; i++)
+#pragma unroll
+                        for (int h = 0; h < 2; h++)
+#pragma unroll
+                            for (int y = 0; y < 2; y++) {
+                                const unsigned bit = (odd >> (4 * i + 2 * h + y)) & 1u ? 1u << gv : 0u;
+                                unsigned all = bit;  // over the lanes of equal t
+                                all |= __shfl_xor_sync(0xFFFFFFFFu, all, 4);
+                                all |= __shfl_xor_sync(0xFFFFFFFFu, all, 8);
+                                all |= __shfl_xor_sync(0xFFFFFFFFu, all, 16);
+                                if (gl == 0) s_odd[kv & 3][(2 * w + i) * kBlk + 8 * h + 2 * t + y] = (uint8_t)all;
+                            }
+                } else {
+                    s_odd[kv & 3][2 * w * kBlk + lane] = 0;
+                }
+                const float km = fmaxf(fmaxf(s_emax[j & 1][0][0], s_emax[j & 1][0][1]), fmaxf(s_emax[j & 1][0][2], s_emax[j & 1][0][3]));
+                const float vm = fmaxf(fmaxf(s_emax[j & 1][1][0], s_emax[j & 1][1][1]), fmaxf(s_emax[j & 1][1][2], s_emax[j & 1][1][3]));
+                // K: the tile's largest of 15 s and |m| goes to [2^8, 2^9), so 1024 s stays in binary16
+                const int ek = max((int)(__float_as_uint(km) >> 23) - 127, -110) - 8;
+                sig = max(sig, (int)(__float_as_uint(vm) >> 23) - 127);
+                if (w == 0 && lane == 0) {
+                    info->ek = ek;
+                    info->ev = sig;
+                }
+                const float kf = pow2f(-ek);
+                uint8_t *kd = sm + S::kK + st * S::kKStage, *kn = sm + S::kKN + st * 4096;
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int row = (2 * w + i) * kBlk + 8 * h + gl;
+                        unsigned ms[NG];
+#pragma unroll
+                        for (int c = 0; c < NG; c++) {
+                            const float s = bits_to_float<BF>(kp[i][h][c] & 0xFFFFu) * kf, m = bits_to_float<BF>(kp[i][h][c] >> 16) * kf;
+                            ms[c] = pack_half(m, m) & 0xFFFFu;
+                            const unsigned s1 = pack_half(s, s), s16 = pack_half(s * 0.0625f, s * 0.0625f);
+                            const unsigned z1 = pack_half(s * -1024.0f, s * -1024.0f), z16 = pack_half(s * -64.0f, s * -64.0f);
+#pragma unroll
+                            for (int x = c * G / 32; x < (c + 1) * G / 32; x++) {
+                                // 1024 + c and 1024 + 16 c as bits; times s, less 1024 s (64 s): s c, exactly
+                                const unsigned u0 = kr[i][h][x], u1 = u0 >> 8;
+                                uint4 y;
+                                y.x = fma_half((u0 & 0x000F000Fu) | 0x64006400u, s1, z1);
+                                y.y = fma_half((u0 & 0x00F000F0u) | 0x64006400u, s16, z16);
+                                y.z = fma_half((u1 & 0x000F000Fu) | 0x64006400u, s1, z1);
+                                y.w = fma_half((u1 & 0x00F000F0u) | 0x64006400u, s16, z16);
+                                *reinterpret_cast<uint4 *>(kd + (x >> 1) * 16384 + row * 128 + (((2 * t + (x & 1)) ^ (row & 7)) << 4)) = y;
+                            }
+                        }
+                        if (t < 2) {  // minima: channels 0..NG-1 and once more, 8 a lane
+                            unsigned o8[4];
+#pragma unroll
+                            for (int c = 0; c < 4; c++) {
+                                unsigned lo = 0, hi = 0;
+#pragma unroll
+                                for (int e = 0; e < 2 * NG; e++) {
+                                    if (e == 8 * t + 2 * c) lo = ms[e % NG];
+                                    if (e == 8 * t + 2 * c + 1) hi = ms[e % NG];
+                                }
+                                o8[c] = lo | (hi << 16);
+                            }
+                            *reinterpret_cast<uint4 *>(kn + (row >> 3) * 256 + t * 128 + (row & 7) * 16) = make_uint4(o8[0], o8[1], o8[2], o8[3]);
+                        }
+                    }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bar_arrive(k_full + 8 * st);
+
+                wait(v_empty + 8 * st, par);
+                const float vf = pow2f(17 - sig);
+                uint8_t *vd = sm + S::kV + st * S::kKStage;
+                constexpr int VW = D / 64, M = 8 / NB;  // words of a token's piece, pieces a block of 64 channels
+#pragma unroll
+                for (int i = 0; i < 2; i++)
+#pragma unroll
+                    for (int h = 0; h < 2; h++)
+#pragma unroll
+                        for (int y = 0; y < 2; y++) {
+                            const int row = (2 * w + i) * kBlk + 8 * h + 2 * t + y;
+                            const float s = bits_to_float<BF>(vp[i][h][y] & 0xFFFFu) * vf;
+                            const float m = bits_to_float<BF>(vp[i][h][y] >> 16) * 5.9604644775390625e-8f * vf;
+                            const unsigned s1 = pack_half(s, s), s16 = pack_half(s * 0.0625f, s * 0.0625f), mm = pack_half(m, m);
+#pragma unroll
+                            for (int x = 0; x < VW; x++) {
+                                const unsigned u0 = vr[i][h][y * VW + x], u1 = u0 >> 8;
+                                uint4 z;
+                                z.x = fma_half(u0 & 0x000F000Fu, s1, mm);
+                                z.y = fma_half(u0 & 0x00F000F0u, s16, mm);
+                                z.z = fma_half(u1 & 0x000F000Fu, s1, mm);
+                                z.w = fma_half(u1 & 0x00F000F0u, s16, mm);
+                                const int chunk = (gl % M) + M * x;
+                                *reinterpret_cast<uint4 *>(vd + (gl / M) * 16384 + row * 128 + ((chunk ^ (row & 7)) << 4)) = z;
+                            }
+                        }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                bar_arrive(v_full + 8 * st);
+                if (j + 1 < n_tiles) fetch(j + 1, pg_next);
+                pg_next = page_at(j + 2);
+            }
+        } else if (q < nq) {
+            // ---- softmax of one row
+            const unsigned ts = tmem + kS0 + q * kKT + ((unsigned)(warp & 3) << 21), to = tmem + kO0 + q * D + ((unsigned)(warp & 3) << 21);
+            const long long pos = g.pos0 + irow;
+            const int hi = mine ? (int)(pos < g.len ? pos : (long long)g.len - 1) : -1;
+            const int lo = mine && a.window && pos + 1 > a.window ? (int)(pos + 1 - a.window) : 0;
+            const int hi_w = __reduce_min_sync(0xFFFFFFFFu, mine ? hi : 0x7FFFFFFF), lo_w = __reduce_max_sync(0xFFFFFFFFu, lo);
+            float m = -INFINITY, l = 0.0f;
+            unsigned bits = 0;
+            int ev = 0;
+            for (int j = 0; j < n_tiles; j++) {
+                const unsigned kv = n_kv + j;
+                wait(s_full + 8 * q, (n_q[q] + j) & 1);
+                fence_after();
+                const volatile Info *info = &s_info[kv & 3];
+                const int tok = (tile0 + j) * kKT, evj = info->ev;
+                const unsigned valid = info->valid;
+                const float f = factor * pow2f(info->ek);
+                const bool plain = valid == 0xFFu && tok >= lo_w && tok + kKT - 1 <= hi_w;
+                unsigned x[32];
+                auto hide = [&](int c) {
+#pragma unroll
+                    for (int i = 0; i < 32; i++) {
+                        const int at = tok + 32 * c + i;
+                        if (at > hi || at < lo || !((valid >> (2 * c + i / 16)) & 1u)) x[i] = 0xFF800000u;
+                    }
+                };
+                float top = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    tmem_ld32(ts + 32 * c, x);
+                    ld_wait();
+                    if (!plain) hide(c);
+#pragma unroll
+                    for (int i = 0; i < 32; i++) top = fmaxf(top, __uint_as_float(x[i]));
+                }
+                top = top == -INFINITY ? top : top * f;
+                const bool raise = top > m + 8.0f;
+                if (__any_sync(0xFFFFFFFFu, raise || evj != ev)) {
+                    const float nm = raise ? top : m;
+                    if (j > 0) {
+                        const float al = (nm == m ? 1.0f : ex2(m - nm)) * (ev - evj < -126 ? 0.0f : pow2f(ev - evj));
+                        l *= nm == m ? 1.0f : ex2(m - nm);
+                        wait(o_done + 8 * q, (n_q[q] + j - 1) & 1);
+                        fence_after();
+#pragma unroll
+                        for (int c = 0; c < D / 32; c++) {
+                            tmem_ld32(to + 32 * c, x);
+                            ld_wait();
+#pragma unroll
+                            for (int i = 0; i < 32; i++) x[i] = __float_as_uint(__uint_as_float(x[i]) * al);
+                            tmem_st32(to + 32 * c, x);
+                        }
+                        st_wait();
+                    }
+                    m = nm;
+                    ev = evj;
+                }
+                if (info->odd) {  // rare: which columns' groups are not finite, for the keys this row sees
+                    for (int c = 0; c < kKT; c++) {
+                        const int at = tok + c;
+                        if (mine && at <= hi && at >= lo && ((valid >> (c / 16)) & 1u)) bits |= *(volatile uint8_t *)&s_odd[kv & 3][c];
+                    }
+                }
+                const float base = m == -INFINITY ? 0.0f : m;
+                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                for (int c = 0; c < 4; c++) {
+                    tmem_ld32(ts + 32 * c, x);
+                    ld_wait();
+                    if (!plain) hide(c);
+                    unsigned y[16];
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        const float e0 = ex2(fmaf(__uint_as_float(x[2 * i]), f, -base)), e1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), f, -base));
+                        acc[i & 1] += e0;
+                        acc[2 + (i & 1)] += e1;
+                        y[i] = pack_half(e0, e1);
+                    }
+                    tmem_st16(ts + 16 * c, y);
+                }
+                l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
+                st_wait();
+                fence_before();
+                bar_arrive(p_full + 8 * q);
+            }
+            // ---- results
+            wait(o_done + 8 * q, (n_q[q] + n_tiles - 1) & 1);
+            fence_after();
+            const float up = pow2f(ev);
+            float *part = partials + ((long long)blockIdx.x * 2 + (g.ua == 0 ? 1 : 0)) * partial_floats<D>();
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            uint16_t *dst = a.out + (long long)(g.first + irow) * a.out_stride + (long long)head * D;
+#pragma unroll
+            for (int c = 0; c < D / 32; c++) {
+                unsigned x[32];
+                tmem_ld32(to + 32 * c, x);
+                ld_wait();
+#pragma unroll
+                for (int i = 0; i < 32; i++) x[i] = __float_as_uint(__uint_as_float(x[i]) * 128.0f * up);
+                if (g.whole) {
+                    if (mine) {
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            constexpr int M = 8 / NB;
+                            const int cb = (4 * c + i) / 8, chunk = (4 * c + i) % 8;
+                            const int d = (cb * M + chunk % M) * (D / 8) + 8 * (chunk / M);
+                            unsigned o4[4];
+#pragma unroll
+                            for (int e = 0; e < 4; e++) {
+                                // channels 2e, 2e + 1 of the eight; their columns are in the order 0 4 1 5 2 6 3 7
+                                const int c0 = 2 * e < 4 ? 4 * e : 4 * (e - 2) + 1, c1 = 2 * e + 1 < 4 ? 4 * e + 2 : 4 * (e - 2) + 3;
+                                float v0 = __uint_as_float(x[8 * i + c0]) * inv, v1 = __uint_as_float(x[8 * i + c1]) * inv;
+                                if ((bits >> (d / G)) & 1u) v0 = v1 = __uint_as_float(0x7FC00000u);
+                                o4[e] = float_to_bits<BF>(v0) | (float_to_bits<BF>(v1) << 16);
+                            }
+                            if (a.out_vec16) {
+                                *reinterpret_cast<uint4 *>(dst + d) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+                            } else {
+#pragma unroll
+                                for (int e = 0; e < 4; e++) {
+                                    dst[d + 2 * e] = (uint16_t)o4[e];
+                                    dst[d + 2 * e + 1] = (uint16_t)(o4[e] >> 16);
+                                }
+                            }
+                        }
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        *reinterpret_cast<uint4 *>(part + ((long long)(8 * c + i) * kRows + q * 128 + r) * 4) =
+                            make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                }
+            }
+            if (g.whole) {
+                if (mine && a.lse)
+                    a.lse[(long long)(g.first + irow) * a.Hq + head] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * kLn2 + logf(l);
+            } else {
+                float *tail = part + kRows * D + q * 128 + r;
+                tail[0] = m;
+                tail[kRows] = l;
+                tail[2 * kRows] = __uint_as_float(bits);
+            }
+            fence_before();
+        }
+
+        // ---- an item of several CTAs: the last one joins
+        if (!g.whole) {
+            const long long c0 = cta_of(g.item_u0, total, grid), c1 = cta_of(g.item_u1 - 1, total, grid);
+            const int count = (int)(c1 - c0 + 1);
+            __threadfence();
+            __syncthreads();
+            if (threadIdx.x == 0) {
+                const unsigned was = atomicAdd(tickets + c0, 1u);
+                s_last = was == (unsigned)(count - 1);
+                if (s_last) tickets[c0] = 0;
+            }
+            __syncthreads();
+            if (s_last && mine) {
+                __threadfence();
+                auto part_of = [&](int k) { return partials + ((c0 + k) * 2 + (k == 0 ? 1 : 0)) * partial_floats<D>(); };
+                const int at = q * 128 + r;
+                float top = -INFINITY;
+                for (int k = 0; k < count; k++) top = fmaxf(top, __ldcg(part_of(k) + kRows * D + at));
+                const float base = top == -INFINITY ? 0.0f : top;
+                float l = 0.0f;
+                unsigned bits = 0;
+                for (int k = 0; k < count; k++) {
+                    const float *tail = part_of(k) + kRows * D + at;
+                    l += __ldcg(tail + kRows) * ex2(__ldcg(tail) - base);
+                    bits |= __float_as_uint(__ldcg(tail + 2 * kRows));
+                }
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                uint16_t *dst = a.out + (long long)(g.first + irow) * a.out_stride + (long long)head * D;
+                for (int c8 = 0; c8 < D / 8; c8++) {  // eight columns: eight channels
+                    float x[8];
+#pragma unroll
+                    for (int i = 0; i < 8; i++) x[i] = 0.0f;
+                    for (int k = 0; k < count; k++) {
+                        const float *src = part_of(k);
+                        const float f = ex2(__ldcg(src + kRows * D + at) - base);
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + ((long long)(2 * c8) * kRows + at) * 4));
+                        const float4 z = __ldcg(reinterpret_cast<const float4 *>(src + ((long long)(2 * c8 + 1) * kRows + at) * 4));
+                        x[0] += y.x * f, x[1] += y.y * f, x[2] += y.z * f, x[3] += y.w * f;
+                        x[4] += z.x * f, x[5] += z.y * f, x[6] += z.z * f, x[7] += z.w * f;
+                    }
+                    constexpr int M = 8 / NB;
+                    const int cb = c8 / 8, chunk = c8 % 8, d = (cb * M + chunk % M) * (D / 8) + 8 * (chunk / M);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        const float v = (bits >> (d / G)) & 1u ? __uint_as_float(0x7FC00000u) : x[i] * inv;
+                        dst[d + (i & 1 ? 4 + i / 2 : i / 2)] = (uint16_t)float_to_bits<BF>(v);
+                    }
+                }
+                if (a.lse) a.lse[(long long)(g.first + irow) * a.Hq + head] = l == 0.0f ? -INFINITY : base * kLn2 + logf(l);
+            }
+        }
+        n_kv += n_tiles;
+        n_q[0] += n_tiles;
+        if (nq == 2) n_q[1] += n_tiles;
+        u += n_tiles;
+    }
+    __syncthreads();
+    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+}
+
+constexpr int kMaxGrid = 256;
+
+template <int D, int G, bool BF>
+cudaError_t chunk_go(const Kv4 &p, const Kv4Attend &a, cudaStream_t s) {
+    static bool ready = false;
+    if (!ready) {
+        const cudaError_t e = cudaFuncSetAttribute(k_kv4_chunk<D, G, BF>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+        if (e != cudaSuccess) return e;
+        ready = true;
+    }
+    int grid = device_sm_count();
+    if (grid > kMaxGrid) grid = kMaxGrid;
+    if (grid < 1) return cudaErrorInvalidDevice;
+    k_kv4_chunk<D, G, BF><<<grid, kThreads, Smem<D>::kBytes, s>>>(p, a);
+    return cudaGetLastError();
+}
+
+template <int D, int G>
+cudaError_t chunk_dg(const Kv4 &p, const Kv4Attend &a, cudaStream_t s) {
+    return p.dtype == CG_DT_BF16 ? chunk_go<D, G, true>(p, a, s) : chunk_go<D, G, false>(p, a, s);
+}
+
+}  // namespace
+
+uint64_t kv4_chunk_workspace_bytes(const Kv4 &p) {
+    return kv4_ticket_bytes() + 2ull * kMaxGrid * 4 * ((uint64_t)kRows * p.D + 3 * kRows);
+}
+
+cudaError_t launch_kv4_chunk(const Kv4 &p, const Kv4Attend &a, cudaStream_t s) {
+    switch (p.D * 1000 + p.G) {
+        case 64032: return chunk_dg<64, 32>(p, a, s);
+        case 64064: return chunk_dg<64, 64>(p, a, s);
+        case 128032: return chunk_dg<128, 32>(p, a, s);
+        case 128064: return chunk_dg<128, 64>(p, a, s);
+        case 128128: return chunk_dg<128, 128>(p, a, s);
+        default: return cudaErrorInvalidValue;
+    }
+}
+
+}  // namespace cg

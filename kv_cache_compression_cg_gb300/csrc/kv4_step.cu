@@ -82,6 +82,7 @@ struct Seq {
 __device__ __forceinline__ Seq seq_of(const Kv4 &p, const Kv4Attend &a, int b, int cols, int32_t *status) {
     Seq s;
     seq_rows(p, b, s.first, s.n, status);
+    if ((long long)s.n * a.R > a.step_max) s.n = 0;
     s.len = s.n ? seq_len(p, b, status) : 0;
     s.u0 = 0;
     s.units = 0;
