@@ -4,9 +4,11 @@
 // A work item is 256 rows (two tiles of 128; a row is a (row of the batch, query head) pair that shares the KV
 // head) against the key tiles of 128 tokens that they see. Warps of a CTA:
 //   0-3, 4-7   softmax of either row tile: a thread owns a row, that is a lane of tensor memory
-//   8-11       K and V: codes and parameters from the pool to registers (a tile ahead), to binary16 in
-//              shared memory, two stages
-//   12         issues the matrix instructions
+//   8-15       K and V: a record a warp, codes and parameters from the pool to registers (ahead), to binary16
+//              in shared memory, two stages
+//   16         issues the matrix instructions
+//   17         finds the work
+// Registers go where they are needed (setmaxnreg): 152 a softmax thread, which holds its row's 128 scores.
 // While one tile's softmax runs the tensor cores work for the other one:
 //   ... P0 V, Q0 K', P1 V, Q1 K', ...
 // Rounding. K goes in as s c, exact in binary16 (seven bits times four) under a power of two of the tile; the
@@ -24,7 +26,8 @@ namespace {
 
 constexpr int kKT = 128;          // keys a tile
 constexpr int kRows = 256;        // rows an item
-constexpr int kThreads = 13 * 32;
+constexpr int kThreads = 20 * 32;
+constexpr int kRegsSoftmax = 152, kRegsStore = 72, kRegsRest = 32;  // x 256, 256, 128 threads: the launch's 640 x 96
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kMaxF = 3.402823466e38f;
 constexpr int kSigMin = -110;
@@ -49,29 +52,61 @@ __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ void mma_ss(unsigned d, uint64_t a, uint64_t b, unsigned idesc, bool add) {
+// Issued by the whole warp's one elected lane (issue != 0): control flow stays uniform, so operands stay in uniform registers.
+// The descriptors' upper word is the same for all matrices of a kind.
+__device__ __forceinline__ void mma_ss(unsigned d, unsigned a, unsigned b, unsigned hi, unsigned idesc, bool add, unsigned issue) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((unsigned)add)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((unsigned)add), "r"(issue)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(unsigned d, unsigned a, uint64_t b, unsigned idesc, bool add) {
+__device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned b, unsigned hi, unsigned idesc, bool add, unsigned issue) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((unsigned)add)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "mov.b64 y, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((unsigned)add), "r"(issue)
         : "memory");
 }
-__device__ __forceinline__ void mma_commit(unsigned bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+__device__ __forceinline__ void mma_commit(unsigned bar, unsigned issue) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(issue)
+        : "memory");
+}
+template <int N>
+__device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+__device__ __forceinline__ void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+// two binary32 side by side
+__device__ __forceinline__ uint64_t pair_of(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void split(uint64_t r, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r)); }
+__device__ __forceinline__ uint64_t fma_pair(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add_pair(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-#define CG_R8(f, o) f[o], f[o + 1], f[o + 2], f[o + 3], f[o + 4], f[o + 5], f[o + 6], f[o + 7]
 __device__ __forceinline__ void tmem_ld32(unsigned addr, unsigned *r) {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -83,14 +118,12 @@ __device__ __forceinline__ void tmem_ld32(unsigned addr, unsigned *r) {
         : "r"(addr)
         : "memory");
 }
-__device__ __forceinline__ void tmem_st32(unsigned addr, const unsigned *r) {
+__device__ __forceinline__ void tmem_ld16(unsigned addr, unsigned *r) {
     asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,"
-        "%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(addr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
-        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
-        "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
-        "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(addr)
         : "memory");
 }
 __device__ __forceinline__ void tmem_st16(unsigned addr, const unsigned *r) {
@@ -101,18 +134,14 @@ __device__ __forceinline__ void tmem_st16(unsigned addr, const unsigned *r) {
         : "memory");
 }
 
-// Shared memory matrix: rows (K-major) or tokens (MN-major) of 128 bytes in blocks of 8, swizzled by 128 bytes;
-// lead: bytes between 64-channel blocks along the contiguous side of an MN-major matrix.
-__device__ __forceinline__ uint64_t desc128(unsigned addr, unsigned lead) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(lead >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           (1ull << 46) | (2ull << 61);
-}
+// Matrices in shared memory: rows (K-major) or tokens (MN-major) of 128 bytes in blocks of 8, 1024 bytes, swizzled by
+// 128 bytes; lead: bytes between 64-channel blocks along the contiguous side of an MN-major matrix.
+constexpr unsigned kHi128 = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ unsigned lo128(unsigned addr, unsigned lead) { return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16); }
 // 16 channels a row, without swizzle: blocks of 8 rows x 16 bytes, 128 bytes each; the two blocks of 8 channels
 // are 128 bytes apart, blocks of 8 rows 256.
-__device__ __forceinline__ uint64_t desc_narrow(unsigned addr) {
-    return (uint64_t)((addr & 0x3FFFFu) >> 4) | ((uint64_t)(128 >> 4) << 16) | ((uint64_t)(256 >> 4) << 32) |
-           (1ull << 46);
-}
+constexpr unsigned kHiNarrow = (256 >> 4) | (1u << 14);
+__device__ __forceinline__ unsigned lo_narrow(unsigned addr) { return lo128(addr, 128); }
 // kind::f16, binary16 in, binary32 out, M = 128.
 __host__ __device__ constexpr unsigned idesc_f16(int n, bool b_mn) {
     return (1u << 4) | ((unsigned)b_mn << 16) | ((unsigned)(n >> 3) << 17) | (8u << 24);
@@ -155,10 +184,13 @@ struct Info {
 };
 
 struct Segment {
-    int b, kvh, row0, first, n, len, t0, tiles, ua, ub, whole;
+    int more;                 // 0: no work is left
+    int b, kvh, row0;         // sequence, KV head, first row of the pair
+    int first, n, len;        // as Span
     long long pos0;
-    long long item_u0, item_u1;
-    int more;
+    int tile0, tiles;         // key tiles of this CTA
+    int begins, whole;        // the item begins here; and ends here
+    int cta0, count;          // CTAs that share it
 };
 
 // The sequence's rows for this kernel, and per row tile pair its key tiles.
@@ -214,14 +246,15 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     using S = Smem<D>;
     constexpr int NG = R::NG, W = D / 32, NB = D / 64;
     constexpr int kS0 = 0, kO0 = 256;  // columns of tensor memory: S of either tile 128, O of either D
+    constexpr int M = 8 / NB;          // pieces of V a block of 64 channels
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[16];
     __shared__ unsigned s_tmem, s_stop, s_last;
     __shared__ Info s_info[4];
     __shared__ uint8_t s_odd[4][kKT];  // bits of a token's value groups that are not finite
-    __shared__ float s_emax[2][2][4];
+    __shared__ float s_emax[2][2][8];
     __shared__ Segment s_seg;
-    __shared__ long long s_sum[13];
+    __shared__ long long s_sum[kThreads / 32];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     uint8_t *sm = raw + ((1024 - (saddr(raw) & 1023)) & 1023);
@@ -230,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     const unsigned k_full = bb, k_empty = bb + 16, v_full = bb + 32, v_empty = bb + 48, s_full = bb + 64, p_full = bb + 80,
                    o_done = bb + 96;  // two of each
 
-    // ---- how much work there is, and where this CTA's range begins
+    // ---- how much work there is
     long long sum = 0;
     for (int b = threadIdx.x; b < p.B; b += kThreads) sum += units_of(p, a, b, a.status);
 #pragma unroll
@@ -239,9 +272,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     if (threadIdx.x == 0) {
         s_stop = 0;
         for (int i = 0; i < 2; i++) {
-            bar_init(k_full + 8 * i, 128);
+            bar_init(k_full + 8 * i, 256);
             bar_init(k_empty + 8 * i, 1);
-            bar_init(v_full + 8 * i, 128);
+            bar_init(v_full + 8 * i, 256);
             bar_init(v_empty + 8 * i, 1);
             bar_init(s_full + 8 * i, 1);
             bar_init(p_full + 8 * i, 128);
@@ -251,38 +284,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     }
     __syncthreads();
     long long total = 0;
-    for (int i = 0; i < 13; i++) total += s_sum[i];
+    for (int i = 0; i < kThreads / 32; i++) total += s_sum[i];
     const long long grid = total < gridDim.x ? total : gridDim.x;
     if (blockIdx.x >= grid) return;
-    long long u = total * blockIdx.x / grid;
-    const long long u_end = total * (blockIdx.x + 1) / grid;
-
-    if (warp == 12) {
+    if (warp == 16) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(&s_tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
         fence_before();
-    }
-    // the sequence that unit u belongs to; kept by warp 0
-    int cur_b = 0;
-    long long before = 0;
-    if (warp == 0) {
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            const long long x = b0 + lane < p.B ? units_of(p, a, b0 + lane, nullptr) : 0;
-            long long incl = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + incl > u);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                cur_b = b0 + src;
-                before += __shfl_sync(0xFFFFFFFFu, incl - x, src);
-                break;
-            }
-            before += __shfl_sync(0xFFFFFFFFu, incl, 31);
-        }
     }
     __syncthreads();
     fence_after();
@@ -299,258 +307,236 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             }
         }
     };
+    // Each role runs the same rounds, one a segment: (a) the last one is over, (b) its description is there, (c) its queries
+    // are in place, then where an item is shared (d) partial results are out, (e) the ticket is drawn.
+    unsigned n_kv = 0;         // key tiles this CTA has begun: stage and parity of K, V
+    unsigned n_q0 = 0, n_q1 = 0;  // tiles of S, P, O of either row tile
 
-    unsigned *tickets = static_cast<unsigned *>(a.ws);
-    float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + a.ticket_bytes);
-    unsigned n_kv = 0;       // key tiles this CTA has begun: stage and parity of K, V
-    unsigned n_q[2] = {0, 0};  // tiles of S, P, O of either row tile
-
-    while (u < u_end) {
-        // ---- the item of unit u
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            Segment g;
-            long long all = units_of(p, a, cur_b, nullptr);
-            while (u - before >= all) {
-                before += all;
-                cur_b++;
-                all = units_of(p, a, cur_b, nullptr);
-            }
-            const Span s = span_of(p, a, cur_b, nullptr);
-            const long long per = all / p.H;
-            long long rest = (u - before) % per;
-            g.b = cur_b;
-            g.kvh = (int)((u - before) / per);
-            int pair = 0;
-            tiles_of(s, a, 0, g.t0, g.tiles);
-            while (rest >= g.tiles) {
-                rest -= g.tiles;
-                tiles_of(s, a, ++pair, g.t0, g.tiles);
-            }
-            g.row0 = pair * kRows;
-            g.first = s.first;
-            g.n = s.n;
-            g.len = s.len;
-            g.pos0 = s.pos0;
-            g.ua = (int)rest;
-            g.ub = u_end - u < g.tiles - rest ? (int)(rest + u_end - u) : g.tiles;
-            g.whole = g.ua == 0 && g.ub == g.tiles;
-            g.item_u0 = u - rest;
-            g.item_u1 = g.item_u0 + g.tiles;
-            s_seg = g;
-        }
-        __syncthreads();
-        const Segment g = s_seg;
-        const int n_rows = g.n * a.R - g.row0;               // of this pair; may pass 256
-        const int nq = n_rows > 128 ? 2 : 1;
-        const int tile0 = g.t0 + g.ua, n_tiles = g.ub - g.ua;
-
-        // ---- queries: row r of the pair, under 2^kq of its own; a chunk of 16 bytes holds channels 32w + 4t + 0..3 and
-        // 16 more on, w = 2 block + chunk % 2, t = chunk / 2: the order K's chunks come in
-        const int q = warp >> 2;                               // softmax warps: their tile
-        const int r = threadIdx.x & 127, rho = g.row0 + q * 128 + r;
-        const bool mine = warp < 8 && rho < g.n * a.R;
-        const int irow = rho / a.R, head = g.kvh * a.R + rho % a.R;
-        float factor = 0.0f;
-        if (warp < 8) {
-            const uint16_t *src = a.q + (long long)(g.first + irow) * a.q_stride + (long long)head * D;
-            auto four = [&](int d, unsigned &x, unsigned &y) {
-                x = y = 0;
-                if (!mine) return;
-                if (a.q_vec) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(src + d);
-                    x = w.x;
-                    y = w.y;
-                } else {
-                    x = src[d] | ((unsigned)src[d + 1] << 16);
-                    y = src[d + 2] | ((unsigned)src[d + 3] << 16);
+    if (warp >= 16) {
+        regs_less<kRegsRest>();
+        const bool finder = warp == 17;
+        long long u = total * blockIdx.x / grid;
+        const long long u_end = total * (blockIdx.x + 1) / grid;
+        int cur_b = 0;
+        long long before = 0, all = 0;  // units of the sequences before cur_b, and of cur_b
+        if (finder) {
+            for (int b0 = 0; b0 < p.B; b0 += 32) {
+                const long long x = b0 + lane < p.B ? units_of(p, a, b0 + lane, nullptr) : 0;
+                long long incl = x;
+#pragma unroll
+                for (int o = 1; o < 32; o <<= 1) {
+                    const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                    if (lane >= o) incl += y;
                 }
-            };
-            float top = 0.0f;
-#pragma unroll 8
-            for (int d = 0; d < D; d += 4) {
-                unsigned x, y;
-                four(d, x, y);
-                top = fmaxf(top, fmaxf(fmaxf(fabsf(bits_to_float<BF>(x & 0xFFFFu)), fabsf(bits_to_float<BF>(x >> 16))),
-                                       fmaxf(fabsf(bits_to_float<BF>(y & 0xFFFFu)), fabsf(bits_to_float<BF>(y >> 16)))));
-            }
-            // the row's largest goes to [2^7, 2^8): sums over a group stay below 2^15
-            int kq = top > 0.0f ? 7 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
-            kq = kq > 120 ? 120 : kq;
-            const float f = a.scale < 0.0f ? -pow2f(kq) : pow2f(kq);
-            factor = fabsf(a.scale) * kLog2e * pow2f(-kq);
-            uint8_t *dst = sm + S::kQ + q * S::kQTile + r * 128;
-            float sums[NG];
-#pragma unroll
-            for (int i = 0; i < NG; i++) sums[i] = 0.0f;
-#pragma unroll
-            for (int c = 0; c < D / 8; c++) {
-                const int block = c / 8, chunk = c % 8, w = 2 * block + (chunk & 1), t = chunk >> 1;
-                unsigned x[4];
-                four(32 * w + 4 * t, x[0], x[1]);
-                four(32 * w + 16 + 4 * t, x[2], x[3]);
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    x[i] = pack_half(bits_to_float<BF>(x[i] & 0xFFFFu) * f, bits_to_float<BF>(x[i] >> 16) * f);
-                    const float2 y = __half22float2(*reinterpret_cast<__half2 *>(&x[i]));
-                    sums[32 * w / G] += y.x + y.y;
+                const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + incl > u);
+                if (hit) {
+                    const int src = __ffs(hit) - 1;
+                    cur_b = b0 + src;
+                    before += __shfl_sync(0xFFFFFFFFu, incl - x, src);
+                    all = __shfl_sync(0xFFFFFFFFu, x, src);
+                    break;
                 }
-                *reinterpret_cast<uint4 *>(dst + block * 16384 + ((chunk ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
+                before += __shfl_sync(0xFFFFFFFFu, incl, 31);
             }
-            // channels 0.. of the narrow block: high parts of the sums, then low parts
-            float nar[16];
-#pragma unroll
-            for (int i = 0; i < 16; i++) nar[i] = 0.0f;
-#pragma unroll
-            for (int i = 0; i < NG; i++) {
-                const float hi = __half2float(__float2half_rn(sums[i]));
-                nar[i] = hi;
-                nar[NG + i] = sums[i] - hi;
-            }
-            uint8_t *nd = sm + S::kQN + q * 4096 + (r >> 3) * 256 + (r & 7) * 16;
-#pragma unroll
-            for (int h = 0; h < 2; h++)
-                *reinterpret_cast<uint4 *>(nd + h * 128) =
-                    make_uint4(pack_half(nar[8 * h], nar[8 * h + 1]), pack_half(nar[8 * h + 2], nar[8 * h + 3]),
-                               pack_half(nar[8 * h + 4], nar[8 * h + 5]), pack_half(nar[8 * h + 6], nar[8 * h + 7]));
-            asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
         }
-        __syncthreads();
-
-        if (warp == 12) {
-            // ---- matrix instructions
-            if (lane == 0) {
+        const unsigned issue = lane == 0;
+        for (;;) {
+            __syncthreads();  // (a)
+            if (finder && lane == 0) {
+                s_seg.more = u < u_end;
+                if (u < u_end) {
+                    while (u - before >= all) {
+                        before += all;
+                        cur_b++;
+                        all = units_of(p, a, cur_b, nullptr);
+                    }
+                    const Span s = span_of(p, a, cur_b, nullptr);
+                    const long long per = all / p.H;
+                    long long rest = (u - before) % per;
+                    int pair = 0, t0, tiles;
+                    tiles_of(s, a, 0, t0, tiles);
+                    while (rest >= tiles) {
+                        rest -= tiles;
+                        tiles_of(s, a, ++pair, t0, tiles);
+                    }
+                    const long long left = u_end - u;
+                    const int here = left < tiles - rest ? (int)left : (int)(tiles - rest);
+                    s_seg.b = cur_b;
+                    s_seg.kvh = (int)((u - before) / per);
+                    s_seg.row0 = pair * kRows;
+                    s_seg.first = s.first;
+                    s_seg.n = s.n;
+                    s_seg.len = s.len;
+                    s_seg.pos0 = s.pos0;
+                    s_seg.tile0 = t0 + (int)rest;
+                    s_seg.tiles = here;
+                    s_seg.begins = rest == 0;
+                    s_seg.whole = here == tiles;
+                    s_seg.cta0 = 0;
+                    s_seg.count = 1;
+                    if (here != tiles) {
+                        s_seg.cta0 = (int)cta_of(u - rest, total, grid);
+                        s_seg.count = (int)cta_of(u - rest + tiles - 1, total, grid) - s_seg.cta0 + 1;
+                    }
+                    u += here;
+                }
+            }
+            __syncthreads();  // (b)
+            if (!s_seg.more) break;
+            const int n_tiles = s_seg.tiles, nq = s_seg.n * a.R - s_seg.row0 > 128 ? 2 : 1;
+            __syncthreads();  // (c)
+            if (warp == 16) {
+                // ---- matrix instructions
                 constexpr unsigned id_s = idesc_f16(kKT, false), id_o = idesc_f16(D, true);
                 auto scores = [&](int i, unsigned kv) {
                     const unsigned st = kv & 1, d = tmem + kS0 + i * kKT;
+                    const unsigned qa = lo128(smb + S::kQ + i * S::kQTile, 16), ka = lo128(smb + S::kK + st * S::kKStage, 16);
 #pragma unroll
                     for (int k = 0; k < D / 16; k++) {
-                        const unsigned off = (k / 4) * 16384 + (k % 4) * 32;
-                        mma_ss(d, desc128(smb + S::kQ + i * S::kQTile + off, 16), desc128(smb + S::kK + st * S::kKStage + off, 16),
-                               id_s, k > 0);
+                        const unsigned off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
+                        mma_ss(d, qa + off, ka + off, kHi128, id_s, k > 0, issue);
                     }
-                    mma_ss(d, desc_narrow(smb + S::kQN + i * 4096), desc_narrow(smb + S::kKN + st * 4096), id_s, true);
-                    mma_commit(s_full + 8 * i);
+                    mma_ss(d, lo_narrow(smb + S::kQN + i * 4096), lo_narrow(smb + S::kKN + st * 4096), kHiNarrow, id_s, true, issue);
+                    mma_commit(s_full + 8 * i, issue);
                 };
                 unsigned kv = n_kv;
                 wait(k_full + 8 * (kv & 1), (kv >> 1) & 1);
                 fence_after();
                 for (int i = 0; i < nq; i++) scores(i, kv);
-                mma_commit(k_empty + 8 * (kv & 1));
+                mma_commit(k_empty + 8 * (kv & 1), issue);
                 for (int j = 0; j < n_tiles; j++, kv++) {
                     wait(v_full + 8 * (kv & 1), (kv >> 1) & 1);
                     for (int i = 0; i < nq; i++) {
-                        wait(p_full + 8 * i, (n_q[i] + j) & 1);
+                        wait(p_full + 8 * i, ((i ? n_q1 : n_q0) + j) & 1);
                         fence_after();
                         const unsigned st = kv & 1, d = tmem + kO0 + i * D, pa = tmem + kS0 + i * kKT;
+                        const unsigned va = lo128(smb + S::kV + st * S::kKStage, 16384);
 #pragma unroll
                         for (int k = 0; k < kKT / 16; k++)
-                            mma_ts(d, pa + 8 * k, desc128(smb + S::kV + st * S::kKStage + k * 2048, 16384), id_o, j > 0 || k > 0);
-                        mma_commit(o_done + 8 * i);
-                        if (i == nq - 1) mma_commit(v_empty + 8 * st);
+                            mma_ts(d, pa + 8 * k, va + k * (2048 >> 4), kHi128, id_o, j > 0 || k > 0, issue);
+                        mma_commit(o_done + 8 * i, issue);
+                        if (i == nq - 1) mma_commit(v_empty + 8 * st, issue);
                         if (j + 1 < n_tiles) {
                             if (i == 0) {
                                 wait(k_full + 8 * ((kv + 1) & 1), ((kv + 1) >> 1) & 1);
                                 fence_after();
                             }
                             scores(i, kv + 1);
-                            if (i == nq - 1) mma_commit(k_empty + 8 * ((kv + 1) & 1));
+                            if (i == nq - 1) mma_commit(k_empty + 8 * ((kv + 1) & 1), issue);
                         }
                     }
                 }
+                __syncwarp();
             }
-            __syncwarp();
-        } else if (warp >= 8) {
-            // ---- K and V of a tile: warp w has records 2w, 2w + 1; lanes as in the step kernel
-            const int w = warp - 8, gl = lane >> 2, t = lane & 3, gv = gl * (D / 8) / G;
-            const int *table = p.table + (long long)g.b * p.max_pages;
-            const int rpp = p.P / kBlk;
-            auto page_at = [&](int j) {  // lanes 0, 1: pages of the warp's records of tile j
+            const bool whole = s_seg.whole;
+            n_kv += n_tiles;
+            n_q0 += n_tiles;
+            if (nq == 2) n_q1 += n_tiles;
+            if (!whole) {
+                __syncthreads();  // (d)
+                if (finder && lane == 0) {
+                    unsigned *tickets = static_cast<unsigned *>(a.ws);
+                    __threadfence();
+                    const unsigned was = atomicAdd(tickets + s_seg.cta0, 1u);
+                    s_last = was == (unsigned)(s_seg.count - 1);
+                    if (s_last) tickets[s_seg.cta0] = 0;
+                }
+                __syncthreads();  // (e)
+            }
+        }
+    } else if (warp >= 8) {
+        regs_less<kRegsStore>();
+        // ---- K and V of the tiles: warp w has record w of each; lanes as in the step kernel
+        const int w = warp - 8, gl = lane >> 2, t = lane & 3, gv = gl * (D / 8) / G;
+        const int rpp = p.P / kBlk;
+        for (;;) {
+            __syncthreads();  // (a)
+            __syncthreads();  // (b)
+            if (!s_seg.more) break;
+            const int tile0 = s_seg.tile0, n_tiles = s_seg.tiles, len = s_seg.len;
+            const int *table = p.table + (long long)s_seg.b * p.max_pages;
+            const uint8_t *heads = a.pool + (long long)s_seg.kvh * rpp * R::kBytes;
+            __syncthreads();  // (c)
+            auto page_at = [&](int j) {  // page of the warp's record of tile j
                 int pg = -1;
-                const long long tok = (long long)(tile0 + j) * kKT + (2 * w + (lane & 1)) * kBlk;
-                if (j < n_tiles && lane < 2 && tok < g.len) {
-                    pg = table[(int)(tok / p.P)];
+                const long long tok = (long long)(tile0 + j) * kKT + w * kBlk;
+                if (j < n_tiles && tok < len) {
+                    pg = __ldg(table + (int)(tok / p.P));
                     if (pg < 0 || pg >= p.pages) {
-                        raise_flag(a.status, CG_FLAG_BATCH);
+                        if (lane == 0) raise_flag(a.status, CG_FLAG_BATCH);
                         pg = -1;
                     }
                 }
                 return pg;
             };
-            unsigned kr[2][2][W], vr[2][2][W], kp[2][2][NG], vp[2][2][2];
-            unsigned ok = 0;
-            auto fetch = [&](int j, int pg) {
-                ok = 0;
+            auto record = [&](int j, int pg) { return heads + pg * p.page_stride + (long long)(((tile0 + j) * (kKT / kBlk) + w) % rpp) * R::kBytes; };
+            unsigned kr[2][W], vr[2][W], kp[2][NG], vp[2][2];
+            auto fetch = [&](unsigned (*x)[W], const uint8_t *src) {
 #pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int page = __shfl_sync(0xFFFFFFFFu, pg, i);
-                    const int rec = (tile0 + j) * (kKT / kBlk) + 2 * w + i;
-                    if (page >= 0) {
-                        ok |= 1u << i;
-                        const uint8_t *src = a.pool + page * p.page_stride + ((long long)g.kvh * rpp + rec % rpp) * R::kBytes;
-#pragma unroll
-                        for (int h = 0; h < 2; h++) {
-                            const uint8_t *kc = src + h * 4 * D + lane * (D / 8), *vc = src + R::kV + h * 4 * D + lane * (D / 8);
-                            if (W == 2) {
-                                const uint2 x = __ldg(reinterpret_cast<const uint2 *>(kc)), y = __ldg(reinterpret_cast<const uint2 *>(vc));
-                                kr[i][h][0] = x.x, kr[i][h][1] = x.y, vr[i][h][0] = y.x, vr[i][h][1] = y.y;
-                            } else {
-#pragma unroll
-                                for (int c = 0; c + 3 < W; c += 4) {
-                                    const uint4 x = __ldg(reinterpret_cast<const uint4 *>(kc) + c / 4);
-                                    const uint4 y = __ldg(reinterpret_cast<const uint4 *>(vc) + c / 4);
-                                    kr[i][h][c] = x.x, kr[i][h][c + 1] = x.y, kr[i][h][c + 2] = x.z, kr[i][h][c + 3] = x.w;
-                                    vr[i][h][c] = y.x, vr[i][h][c + 1] = y.y, vr[i][h][c + 2] = y.z, vr[i][h][c + 3] = y.w;
-                                }
-                            }
-                            const unsigned *pk = reinterpret_cast<const unsigned *>(src + R::kPK) + (8 * h + gl) * NG;
-#pragma unroll
-                            for (int c = 0; c < NG; c++) kp[i][h][c] = __ldg(pk + c);
-                            const unsigned *pv = reinterpret_cast<const unsigned *>(src + R::kPV) + (8 * h + 2 * t) * NG + gv;
-                            vp[i][h][0] = __ldg(pv);
-                            vp[i][h][1] = __ldg(pv + NG);
-                        }
+                for (int h = 0; h < 2; h++) {
+                    const uint8_t *c = src + h * 4 * D + lane * (D / 8);
+                    if (W == 2) {
+                        const uint2 y = __ldg(reinterpret_cast<const uint2 *>(c));
+                        x[h][0] = y.x, x[h][1] = y.y;
                     } else {
-#pragma unroll
-                        for (int h = 0; h < 2; h++) {
-#pragma unroll
-                            for (int c = 0; c < W; c++) kr[i][h][c] = vr[i][h][c] = 0;
-#pragma unroll
-                            for (int c = 0; c < NG; c++) kp[i][h][c] = 0;
-                            vp[i][h][0] = vp[i][h][1] = 0;
-                        }
+                        const uint4 y = __ldg(reinterpret_cast<const uint4 *>(c));
+                        x[h][0] = y.x, x[h][1] = y.y, x[h][2 % W] = y.z, x[h][3 % W] = y.w;
                     }
                 }
             };
-            fetch(0, page_at(0));
-            int pg_next = page_at(1);
+            auto fetch_params = [&](const uint8_t *src, unsigned (*xk)[NG], unsigned (*xv)[2]) {
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const unsigned *pk = reinterpret_cast<const unsigned *>(src + R::kPK) + (8 * h + gl) * NG;
+#pragma unroll
+                    for (int c = 0; c < NG; c++) xk[h][c] = __ldg(pk + c);
+                    const unsigned *pv = reinterpret_cast<const unsigned *>(src + R::kPV) + (8 * h + 2 * t) * NG + gv;
+                    xv[h][0] = __ldg(pv);
+                    xv[h][1] = __ldg(pv + NG);
+                }
+            };
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+#pragma unroll
+                for (int c = 0; c < W; c++) kr[h][c] = vr[h][c] = 0;
+#pragma unroll
+                for (int c = 0; c < NG; c++) kp[h][c] = 0;
+                vp[h][0] = vp[h][1] = 0;
+            }
+            int pg = page_at(0), pg1 = page_at(1);
+            if (pg >= 0) {
+                const uint8_t *src = record(0, pg);
+                fetch_params(src, kp, vp);
+                fetch(kr, src);
+                fetch(vr, src + R::kV);
+            }
             int sig = kSigMin;
             for (int j = 0; j < n_tiles; j++) {
                 const unsigned kv = n_kv + j, st = kv & 1, par = ((kv >> 1) & 1) ^ 1;
-                const int base = (tile0 + j) * kKT + 2 * w * kBlk;
+                const int base = (tile0 + j) * kKT + w * kBlk;
+                const uint8_t *src1 = record(j + 1, pg1);
+                const int pg2 = page_at(j + 2);
                 // parameters of tokens that the sequence does not hold count as zero; a value group that is not finite too
                 // (its rows are found by their bits), a key group's NaN stays
                 float kmax = 0.0f, vmax = 0.0f;
                 unsigned odd = 0;
 #pragma unroll
-                for (int i = 0; i < 2; i++)
+                for (int h = 0; h < 2; h++) {
+                    const bool have = pg >= 0 && base + 8 * h + gl < len;
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        if (base + i * kBlk + 8 * h + gl >= g.len)
-#pragma unroll
-                            for (int c = 0; c < NG; c++) kp[i][h][c] = 0;
-#pragma unroll
-                        for (int c = 0; c < NG; c++)
-                            kmax = fmaxf(kmax, fmaxf(15.0f * bits_to_float<BF>(kp[i][h][c] & 0xFFFFu), fabsf(bits_to_float<BF>(kp[i][h][c] >> 16))));
-#pragma unroll
-                        for (int y = 0; y < 2; y++) {
-                            const float s = bits_to_float<BF>(vp[i][h][y] & 0xFFFFu), m = bits_to_float<BF>(vp[i][h][y] >> 16);
-                            const bool held = base + i * kBlk + 8 * h + 2 * t + y < g.len, fine = fabsf(s) <= kMaxF && fabsf(m) <= kMaxF;
-                            if (held && !fine) odd |= 1u << (4 * i + 2 * h + y);
-                            if (!held || !fine) vp[i][h][y] = 0;
-                            else vmax = fmaxf(vmax, fmaxf(fabsf(m), fabsf(fmaf(15.0f, s, m))));
-                        }
+                    for (int c = 0; c < NG; c++) {
+                        if (!have) kp[h][c] = 0;
+                        kmax = fmaxf(kmax, fmaxf(15.0f * bits_to_float<BF>(kp[h][c] & 0xFFFFu), fabsf(bits_to_float<BF>(kp[h][c] >> 16))));
                     }
+#pragma unroll
+                    for (int y = 0; y < 2; y++) {
+                        const float s = bits_to_float<BF>(vp[h][y] & 0xFFFFu), m = bits_to_float<BF>(vp[h][y] >> 16);
+                        const bool held = pg >= 0 && base + 8 * h + 2 * t + y < len, fine = fabsf(s) <= kMaxF && fabsf(m) <= kMaxF;
+                        if (held && !fine) odd |= 1u << (2 * h + y);
+                        if (!held || !fine) vp[h][y] = 0;
+                        else vmax = fmaxf(vmax, fmaxf(fabsf(m), fabsf(fmaf(15.0f, s, m))));
+                    }
+                }
                 const unsigned ku = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(kmax, kMaxF)));
                 const unsigned vu = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(vmax, kMaxF)));
                 if (lane == 0) {
@@ -565,32 +551,31 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                     info->valid = 0;
                     info->odd = 0;
                 }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
+                asm volatile("bar.sync 1, 256;" ::: "memory");
                 if (lane == 0) {
-                    atomicOr(&info->valid, ok << (2 * w));
+                    if (pg >= 0) atomicOr(&info->valid, 1u << w);
                     if (any_odd) atomicOr(&info->odd, 1u << w);
                 }
                 if (any_odd) {  // rare: bits of each token's groups
-                    s_odd[kv & 3][2 * w * kBlk + lane] = 0;
-                    __syncwarp();
 #pragma unroll
-                    for (int i = 0; i < 2; i++)
+                    for (int h = 0; h < 2; h++)
 #pragma unroll
-                        for (int h = 0; h < 2; h++)
-#pragma unroll
-                            for (int y = 0; y < 2; y++) {
-                                const unsigned bit = (odd >> (4 * i + 2 * h + y)) & 1u ? 1u << gv : 0u;
-                                unsigned all = bit;  // over the lanes of equal t
-                                all |= __shfl_xor_sync(0xFFFFFFFFu, all, 4);
-                                all |= __shfl_xor_sync(0xFFFFFFFFu, all, 8);
-                                all |= __shfl_xor_sync(0xFFFFFFFFu, all, 16);
-                                if (gl == 0) s_odd[kv & 3][(2 * w + i) * kBlk + 8 * h + 2 * t + y] = (uint8_t)all;
-                            }
-                } else {
-                    s_odd[kv & 3][2 * w * kBlk + lane] = 0;
+                        for (int y = 0; y < 2; y++) {
+                            unsigned bits = (odd >> (2 * h + y)) & 1u ? 1u << gv : 0u;  // over the lanes of equal t
+                            bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, 4);
+                            bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, 8);
+                            bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, 16);
+                            if (gl == 0) s_odd[kv & 3][w * kBlk + 8 * h + 2 * t + y] = (uint8_t)bits;
+                        }
+                } else if (lane < kBlk) {
+                    s_odd[kv & 3][w * kBlk + lane] = 0;
                 }
-                const float km = fmaxf(fmaxf(s_emax[j & 1][0][0], s_emax[j & 1][0][1]), fmaxf(s_emax[j & 1][0][2], s_emax[j & 1][0][3]));
-                const float vm = fmaxf(fmaxf(s_emax[j & 1][1][0], s_emax[j & 1][1][1]), fmaxf(s_emax[j & 1][1][2], s_emax[j & 1][1][3]));
+                float km = s_emax[j & 1][0][0], vm = s_emax[j & 1][1][0];
+#pragma unroll
+                for (int i = 1; i < 8; i++) {
+                    km = fmaxf(km, s_emax[j & 1][0][i]);
+                    vm = fmaxf(vm, s_emax[j & 1][1][i]);
+                }
                 // K: the tile's largest of 15 s and |m| goes to [2^8, 2^9), so 1024 s stays in binary16
                 const int ek = max((int)(__float_as_uint(km) >> 23) - 127, -110) - 8;
                 sig = max(sig, (int)(__float_as_uint(vm) >> 23) - 127);
@@ -601,240 +586,331 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                 const float kf = pow2f(-ek);
                 uint8_t *kd = sm + S::kK + st * S::kKStage, *kn = sm + S::kKN + st * 4096;
 #pragma unroll
-                for (int i = 0; i < 2; i++)
+                for (int h = 0; h < 2; h++) {
+                    const int row = w * kBlk + 8 * h + gl;
+                    unsigned ms[NG];
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        const int row = (2 * w + i) * kBlk + 8 * h + gl;
-                        unsigned ms[NG];
+                    for (int c = 0; c < NG; c++) {
+                        const float s = bits_to_float<BF>(kp[h][c] & 0xFFFFu) * kf, m = bits_to_float<BF>(kp[h][c] >> 16) * kf;
+                        ms[c] = pack_half(m, m) & 0xFFFFu;
+                        const unsigned s1 = pack_half(s, s), s16 = pack_half(s * 0.0625f, s * 0.0625f);
+                        const unsigned z1 = pack_half(s * -1024.0f, s * -1024.0f), z16 = pack_half(s * -64.0f, s * -64.0f);
 #pragma unroll
-                        for (int c = 0; c < NG; c++) {
-                            const float s = bits_to_float<BF>(kp[i][h][c] & 0xFFFFu) * kf, m = bits_to_float<BF>(kp[i][h][c] >> 16) * kf;
-                            ms[c] = pack_half(m, m) & 0xFFFFu;
-                            const unsigned s1 = pack_half(s, s), s16 = pack_half(s * 0.0625f, s * 0.0625f);
-                            const unsigned z1 = pack_half(s * -1024.0f, s * -1024.0f), z16 = pack_half(s * -64.0f, s * -64.0f);
-#pragma unroll
-                            for (int x = c * G / 32; x < (c + 1) * G / 32; x++) {
-                                // 1024 + c and 1024 + 16 c as bits; times s, less 1024 s (64 s): s c, exactly
-                                const unsigned u0 = kr[i][h][x], u1 = u0 >> 8;
-                                uint4 y;
-                                y.x = fma_half((u0 & 0x000F000Fu) | 0x64006400u, s1, z1);
-                                y.y = fma_half((u0 & 0x00F000F0u) | 0x64006400u, s16, z16);
-                                y.z = fma_half((u1 & 0x000F000Fu) | 0x64006400u, s1, z1);
-                                y.w = fma_half((u1 & 0x00F000F0u) | 0x64006400u, s16, z16);
-                                *reinterpret_cast<uint4 *>(kd + (x >> 1) * 16384 + row * 128 + (((2 * t + (x & 1)) ^ (row & 7)) << 4)) = y;
-                            }
-                        }
-                        if (t < 2) {  // minima: channels 0..NG-1 and once more, 8 a lane
-                            unsigned o8[4];
-#pragma unroll
-                            for (int c = 0; c < 4; c++) {
-                                unsigned lo = 0, hi = 0;
-#pragma unroll
-                                for (int e = 0; e < 2 * NG; e++) {
-                                    if (e == 8 * t + 2 * c) lo = ms[e % NG];
-                                    if (e == 8 * t + 2 * c + 1) hi = ms[e % NG];
-                                }
-                                o8[c] = lo | (hi << 16);
-                            }
-                            *reinterpret_cast<uint4 *>(kn + (row >> 3) * 256 + t * 128 + (row & 7) * 16) = make_uint4(o8[0], o8[1], o8[2], o8[3]);
+                        for (int x = c * G / 32; x < (c + 1) * G / 32; x++) {
+                            // 1024 + c and 1024 + 16 c as bits; times s, less 1024 s (64 s): s c, exactly
+                            const unsigned u0 = kr[h][x], u1 = u0 >> 8;
+                            uint4 y;
+                            y.x = fma_half((u0 & 0x000F000Fu) | 0x64006400u, s1, z1);
+                            y.y = fma_half((u0 & 0x00F000F0u) | 0x64006400u, s16, z16);
+                            y.z = fma_half((u1 & 0x000F000Fu) | 0x64006400u, s1, z1);
+                            y.w = fma_half((u1 & 0x00F000F0u) | 0x64006400u, s16, z16);
+                            *reinterpret_cast<uint4 *>(kd + (x >> 1) * 16384 + row * 128 + (((2 * t + (x & 1)) ^ (row & 7)) << 4)) = y;
                         }
                     }
+                    if (t < 2) {  // minima: channels 0..NG-1 and once more, 8 a lane
+                        unsigned o8[4];
+#pragma unroll
+                        for (int c = 0; c < 4; c++) {
+                            unsigned lo = 0, hi = 0;
+#pragma unroll
+                            for (int e = 0; e < 2 * NG; e++) {
+                                if (e == 8 * t + 2 * c) lo = ms[e % NG];
+                                if (e == 8 * t + 2 * c + 1) hi = ms[e % NG];
+                            }
+                            o8[c] = lo | (hi << 16);
+                        }
+                        *reinterpret_cast<uint4 *>(kn + (row >> 3) * 256 + t * 128 + (row & 7) * 16) = make_uint4(o8[0], o8[1], o8[2], o8[3]);
+                    }
+                }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 bar_arrive(k_full + 8 * st);
-
-                wait(v_empty + 8 * st, par);
                 const float vf = pow2f(17 - sig);
+                unsigned vs[2][2], vm2[2][2];  // s and m of tokens 2t, 2t + 1 of either half, scaled
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+#pragma unroll
+                    for (int y = 0; y < 2; y++) {
+                        const float s = bits_to_float<BF>(vp[h][y] & 0xFFFFu) * vf;
+                        const float m = bits_to_float<BF>(vp[h][y] >> 16) * 5.9604644775390625e-8f * vf;
+                        vs[h][y] = pack_half(s, s * 0.0625f);
+                        vm2[h][y] = pack_half(m, m);
+                    }
+                if (pg1 >= 0) {
+                    fetch_params(src1, kp, vp);
+                    fetch(kr, src1);
+                }
+                wait(v_empty + 8 * st, par);
                 uint8_t *vd = sm + S::kV + st * S::kKStage;
-                constexpr int VW = D / 64, M = 8 / NB;  // words of a token's piece, pieces a block of 64 channels
+                constexpr int VW = D / 64;  // words of a token's piece
 #pragma unroll
-                for (int i = 0; i < 2; i++)
+                for (int h = 0; h < 2; h++)
 #pragma unroll
-                    for (int h = 0; h < 2; h++)
+                    for (int y = 0; y < 2; y++) {
+                        const int row = w * kBlk + 8 * h + 2 * t + y;
+                        const unsigned s1 = __byte_perm(vs[h][y], 0, 0x1010), s16 = __byte_perm(vs[h][y], 0, 0x3232), mm = vm2[h][y];
 #pragma unroll
-                        for (int y = 0; y < 2; y++) {
-                            const int row = (2 * w + i) * kBlk + 8 * h + 2 * t + y;
-                            const float s = bits_to_float<BF>(vp[i][h][y] & 0xFFFFu) * vf;
-                            const float m = bits_to_float<BF>(vp[i][h][y] >> 16) * 5.9604644775390625e-8f * vf;
-                            const unsigned s1 = pack_half(s, s), s16 = pack_half(s * 0.0625f, s * 0.0625f), mm = pack_half(m, m);
-#pragma unroll
-                            for (int x = 0; x < VW; x++) {
-                                const unsigned u0 = vr[i][h][y * VW + x], u1 = u0 >> 8;
-                                uint4 z;
-                                z.x = fma_half(u0 & 0x000F000Fu, s1, mm);
-                                z.y = fma_half(u0 & 0x00F000F0u, s16, mm);
-                                z.z = fma_half(u1 & 0x000F000Fu, s1, mm);
-                                z.w = fma_half(u1 & 0x00F000F0u, s16, mm);
-                                const int chunk = (gl % M) + M * x;
-                                *reinterpret_cast<uint4 *>(vd + (gl / M) * 16384 + row * 128 + ((chunk ^ (row & 7)) << 4)) = z;
-                            }
+                        for (int x = 0; x < VW; x++) {
+                            const unsigned u0 = vr[h][y * VW + x], u1 = u0 >> 8;
+                            uint4 z;
+                            z.x = fma_half(u0 & 0x000F000Fu, s1, mm);
+                            z.y = fma_half(u0 & 0x00F000F0u, s16, mm);
+                            z.z = fma_half(u1 & 0x000F000Fu, s1, mm);
+                            z.w = fma_half(u1 & 0x00F000F0u, s16, mm);
+                            const int chunk = (gl % M) + M * x;
+                            *reinterpret_cast<uint4 *>(vd + (gl / M) * 16384 + row * 128 + ((chunk ^ (row & 7)) << 4)) = z;
                         }
+                    }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 bar_arrive(v_full + 8 * st);
-                if (j + 1 < n_tiles) fetch(j + 1, pg_next);
-                pg_next = page_at(j + 2);
+                if (pg1 >= 0) fetch(vr, src1 + R::kV);
+                pg = pg1;
+                pg1 = pg2;
             }
-        } else if (q < nq) {
-            // ---- softmax of one row
-            const unsigned ts = tmem + kS0 + q * kKT + ((unsigned)(warp & 3) << 21), to = tmem + kO0 + q * D + ((unsigned)(warp & 3) << 21);
-            const long long pos = g.pos0 + irow;
-            const int hi = mine ? (int)(pos < g.len ? pos : (long long)g.len - 1) : -1;
-            const int lo = mine && a.window && pos + 1 > a.window ? (int)(pos + 1 - a.window) : 0;
-            const int hi_w = __reduce_min_sync(0xFFFFFFFFu, mine ? hi : 0x7FFFFFFF), lo_w = __reduce_max_sync(0xFFFFFFFFu, lo);
-            float m = -INFINITY, l = 0.0f;
-            unsigned bits = 0;
-            int ev = 0;
-            for (int j = 0; j < n_tiles; j++) {
-                const unsigned kv = n_kv + j;
-                wait(s_full + 8 * q, (n_q[q] + j) & 1);
-                fence_after();
-                const volatile Info *info = &s_info[kv & 3];
-                const int tok = (tile0 + j) * kKT, evj = info->ev;
-                const unsigned valid = info->valid;
-                const float f = factor * pow2f(info->ek);
-                const bool plain = valid == 0xFFu && tok >= lo_w && tok + kKT - 1 <= hi_w;
-                unsigned x[32];
-                auto hide = [&](int c) {
-#pragma unroll
-                    for (int i = 0; i < 32; i++) {
-                        const int at = tok + 32 * c + i;
-                        if (at > hi || at < lo || !((valid >> (2 * c + i / 16)) & 1u)) x[i] = 0xFF800000u;
+            n_kv += n_tiles;
+            if (!s_seg.whole) {
+                __syncthreads();  // (d)
+                __syncthreads();  // (e)
+            }
+        }
+    } else {
+        regs_more<kRegsSoftmax>();
+        const int q = warp >> 2, r = threadIdx.x & 127;  // row tile, row
+        const unsigned ts = tmem + kS0 + q * kKT + ((unsigned)(warp & 3) << 21), to = tmem + kO0 + q * D + ((unsigned)(warp & 3) << 21);
+        float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + a.ticket_bytes);
+        unsigned n_q = 0;
+        for (;;) {
+            __syncthreads();  // (a)
+            __syncthreads();  // (b)
+            if (!s_seg.more) break;
+            const int tile0 = s_seg.tile0, n_tiles = s_seg.tiles, len = s_seg.len;
+            const int rho = s_seg.row0 + q * 128 + r;
+            const bool mine = rho < s_seg.n * a.R, active = q == 0 || s_seg.n * a.R - s_seg.row0 > 128;
+            const int irow = rho / a.R, head = s_seg.kvh * a.R + rho % a.R;
+            const long long out_row = s_seg.first + irow, pos = s_seg.pos0 + irow;
+            float factor = 0.0f;
+            // ---- queries: under 2^kq of the row's own; a chunk of 16 bytes holds channels 32w + 4t + 0..3 and
+            // 16 more on, w = 2 block + chunk % 2, t = chunk / 2: the order K's chunks come in
+            {
+                const uint16_t *src = a.q + out_row * a.q_stride + (long long)head * D;
+                auto four = [&](int d, unsigned &x, unsigned &y) {
+                    x = y = 0;
+                    if (!mine) return;
+                    if (a.q_vec) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(src + d);
+                        x = w.x;
+                        y = w.y;
+                    } else {
+                        x = src[d] | ((unsigned)src[d + 1] << 16);
+                        y = src[d + 2] | ((unsigned)src[d + 3] << 16);
                     }
                 };
-                float top = -INFINITY;
-#pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    tmem_ld32(ts + 32 * c, x);
-                    ld_wait();
-                    if (!plain) hide(c);
-#pragma unroll
-                    for (int i = 0; i < 32; i++) top = fmaxf(top, __uint_as_float(x[i]));
+                float top = 0.0f;
+#pragma unroll 8
+                for (int d = 0; d < D; d += 4) {
+                    unsigned x, y;
+                    four(d, x, y);
+                    top = fmaxf(top, fmaxf(fmaxf(fabsf(bits_to_float<BF>(x & 0xFFFFu)), fabsf(bits_to_float<BF>(x >> 16))),
+                                           fmaxf(fabsf(bits_to_float<BF>(y & 0xFFFFu)), fabsf(bits_to_float<BF>(y >> 16)))));
                 }
-                top = top == -INFINITY ? top : top * f;
-                const bool raise = top > m + 8.0f;
-                if (__any_sync(0xFFFFFFFFu, raise || evj != ev)) {
-                    const float nm = raise ? top : m;
-                    if (j > 0) {
-                        const float al = (nm == m ? 1.0f : ex2(m - nm)) * (ev - evj < -126 ? 0.0f : pow2f(ev - evj));
-                        l *= nm == m ? 1.0f : ex2(m - nm);
-                        wait(o_done + 8 * q, (n_q[q] + j - 1) & 1);
-                        fence_after();
+                // the row's largest goes to [2^7, 2^8): sums over a group stay below 2^15
+                int kq = top > 0.0f ? 7 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
+                kq = kq > 120 ? 120 : kq;
+                const float f = a.scale < 0.0f ? -pow2f(kq) : pow2f(kq);
+                factor = fabsf(a.scale) * kLog2e * pow2f(-kq);
+                uint8_t *dst = sm + S::kQ + q * S::kQTile + r * 128;
+                float sums[NG];
 #pragma unroll
-                        for (int c = 0; c < D / 32; c++) {
-                            tmem_ld32(to + 32 * c, x);
-                            ld_wait();
+                for (int i = 0; i < NG; i++) sums[i] = 0.0f;
 #pragma unroll
-                            for (int i = 0; i < 32; i++) x[i] = __float_as_uint(__uint_as_float(x[i]) * al);
-                            tmem_st32(to + 32 * c, x);
-                        }
-                        st_wait();
+                for (int c = 0; c < D / 8; c++) {
+                    const int block = c / 8, chunk = c % 8, w = 2 * block + (chunk & 1), t = chunk >> 1;
+                    unsigned x[4];
+                    four(32 * w + 4 * t, x[0], x[1]);
+                    four(32 * w + 16 + 4 * t, x[2], x[3]);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        x[i] = pack_half(bits_to_float<BF>(x[i] & 0xFFFFu) * f, bits_to_float<BF>(x[i] >> 16) * f);
+                        const float2 y = __half22float2(*reinterpret_cast<__half2 *>(&x[i]));
+                        sums[32 * w / G] += y.x + y.y;
                     }
-                    m = nm;
-                    ev = evj;
+                    *reinterpret_cast<uint4 *>(dst + block * 16384 + ((chunk ^ (r & 7)) << 4)) = make_uint4(x[0], x[1], x[2], x[3]);
                 }
-                if (info->odd) {  // rare: which columns' groups are not finite, for the keys this row sees
-                    for (int c = 0; c < kKT; c++) {
-                        const int at = tok + c;
-                        if (mine && at <= hi && at >= lo && ((valid >> (c / 16)) & 1u)) bits |= *(volatile uint8_t *)&s_odd[kv & 3][c];
-                    }
-                }
-                const float base = m == -INFINITY ? 0.0f : m;
-                float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                // channels 0.. of the narrow block: high parts of the sums, then low parts
+                float nar[16];
 #pragma unroll
-                for (int c = 0; c < 4; c++) {
-                    tmem_ld32(ts + 32 * c, x);
-                    ld_wait();
-                    if (!plain) hide(c);
-                    unsigned y[16];
+                for (int i = 0; i < 16; i++) nar[i] = 0.0f;
 #pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        const float e0 = ex2(fmaf(__uint_as_float(x[2 * i]), f, -base)), e1 = ex2(fmaf(__uint_as_float(x[2 * i + 1]), f, -base));
-                        acc[i & 1] += e0;
-                        acc[2 + (i & 1)] += e1;
-                        y[i] = pack_half(e0, e1);
-                    }
-                    tmem_st16(ts + 16 * c, y);
+                for (int i = 0; i < NG; i++) {
+                    const float hi = __half2float(__float2half_rn(sums[i]));
+                    nar[i] = hi;
+                    nar[NG + i] = sums[i] - hi;
                 }
-                l += (acc[0] + acc[1]) + (acc[2] + acc[3]);
-                st_wait();
-                fence_before();
-                bar_arrive(p_full + 8 * q);
+                uint8_t *nd = sm + S::kQN + q * 4096 + (r >> 3) * 256 + (r & 7) * 16;
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    *reinterpret_cast<uint4 *>(nd + h * 128) =
+                        make_uint4(pack_half(nar[8 * h], nar[8 * h + 1]), pack_half(nar[8 * h + 2], nar[8 * h + 3]),
+                                   pack_half(nar[8 * h + 4], nar[8 * h + 5]), pack_half(nar[8 * h + 6], nar[8 * h + 7]));
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
-            // ---- results
-            wait(o_done + 8 * q, (n_q[q] + n_tiles - 1) & 1);
-            fence_after();
-            const float up = pow2f(ev);
-            float *part = partials + ((long long)blockIdx.x * 2 + (g.ua == 0 ? 1 : 0)) * partial_floats<D>();
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            uint16_t *dst = a.out + (long long)(g.first + irow) * a.out_stride + (long long)head * D;
+            __syncthreads();  // (c)
+            if (active) {
+                // ---- softmax of the row
+                const int hi = mine ? (int)(pos < len ? pos : (long long)len - 1) : -1;
+                const int lo = mine && a.window && pos + 1 > a.window ? (int)(pos + 1 - a.window) : 0;
+                const int hi_w = __reduce_min_sync(0xFFFFFFFFu, mine ? hi : 0x7FFFFFFF), lo_w = __reduce_max_sync(0xFFFFFFFFu, lo);
+                float m = -INFINITY, l = 0.0f;
+                unsigned bits = 0;
+                int ev = 0;
+                for (int j = 0; j < n_tiles; j++) {
+                    const unsigned kv = n_kv + j;
+                    wait(s_full + 8 * q, (n_q + j) & 1);
+                    fence_after();
+                    unsigned x[kKT];
 #pragma unroll
-            for (int c = 0; c < D / 32; c++) {
-                unsigned x[32];
-                tmem_ld32(to + 32 * c, x);
-                ld_wait();
+                    for (int c = 0; c < 4; c++) tmem_ld32(ts + 32 * c, x + 32 * c);
+                    const volatile Info *info = &s_info[kv & 3];
+                    const int tok = (tile0 + j) * kKT, evj = info->ev;
+                    const unsigned valid = info->valid;
+                    const float f = factor * pow2f(info->ek);
+                    const bool plain = valid == 0xFFu && tok >= lo_w && tok + kKT - 1 <= hi_w;
+                    ld_wait();
+                    if (!plain) {
 #pragma unroll
-                for (int i = 0; i < 32; i++) x[i] = __float_as_uint(__uint_as_float(x[i]) * 128.0f * up);
-                if (g.whole) {
-                    if (mine) {
+                        for (int i = 0; i < kKT; i++) {
+                            const int at = tok + i;
+                            if (at > hi || at < lo || !((valid >> (i / 16)) & 1u)) x[i] = 0xFF800000u;
+                        }
+                    }
+                    float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                        for (int i = 0; i < 4; i++) {
-                            constexpr int M = 8 / NB;
-                            const int cb = (4 * c + i) / 8, chunk = (4 * c + i) % 8;
-                            const int d = (cb * M + chunk % M) * (D / 8) + 8 * (chunk / M);
-                            unsigned o4[4];
+                    for (int i = 0; i < kKT; i += 2) t4[(i / 2) & 3] = max3(t4[(i / 2) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                    float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
+                    top = top == -INFINITY ? top : top * f;
+                    const bool raise = top > m + 8.0f;
+                    if (__any_sync(0xFFFFFFFFu, raise || evj != ev)) {
+                        const float nm = raise ? top : m;
+                        if (j > 0) {
+                            const float fm = nm == m ? 1.0f : ex2(m - nm);
+                            const float al = fm * (ev - evj < -126 ? 0.0f : pow2f(ev - evj));
+                            l *= fm;
+                            wait(o_done + 8 * q, (n_q + j - 1) & 1);
+                            fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                unsigned y[16];
+                                tmem_ld16(to + c, y);
+                                ld_wait();
 #pragma unroll
-                            for (int e = 0; e < 4; e++) {
-                                // channels 2e, 2e + 1 of the eight; their columns are in the order 0 4 1 5 2 6 3 7
-                                const int c0 = 2 * e < 4 ? 4 * e : 4 * (e - 2) + 1, c1 = 2 * e + 1 < 4 ? 4 * e + 2 : 4 * (e - 2) + 3;
-                                float v0 = __uint_as_float(x[8 * i + c0]) * inv, v1 = __uint_as_float(x[8 * i + c1]) * inv;
-                                if ((bits >> (d / G)) & 1u) v0 = v1 = __uint_as_float(0x7FC00000u);
-                                o4[e] = float_to_bits<BF>(v0) | (float_to_bits<BF>(v1) << 16);
+                                for (int i = 0; i < 16; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * al);
+                                tmem_st16(to + c, y);
                             }
-                            if (a.out_vec16) {
-                                *reinterpret_cast<uint4 *>(dst + d) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-                            } else {
+                            st_wait();
+                        }
+                        m = nm;
+                        ev = evj;
+                    }
+                    if (info->odd) {  // rare: which columns' groups are not finite, for the keys this row sees
+#pragma unroll 1
+                        for (int c = 0; c < kKT; c++) {
+                            const int at = tok + c;
+                            if (mine && at <= hi && at >= lo && ((valid >> (c / 16)) & 1u)) bits |= *(volatile uint8_t *)&s_odd[kv & 3][c];
+                        }
+                    }
+                    const float base = m == -INFINITY ? 0.0f : m;
+                    const uint64_t f2 = pair_of(f, f), b2 = pair_of(-base, -base);
+                    uint64_t acc[2] = {0, 0};
+#pragma unroll
+                    for (int c = 0; c < 4; c++) {
+                        unsigned y[16];
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            float e0, e1;
+                            split(fma_pair(pair_of(__uint_as_float(x[32 * c + 2 * i]), __uint_as_float(x[32 * c + 2 * i + 1])), f2, b2), e0, e1);
+                            e0 = ex2(e0);
+                            e1 = ex2(e1);
+                            acc[i & 1] = add_pair(acc[i & 1], pair_of(e0, e1));
+                            y[i] = pack_half(e0, e1);
+                        }
+                        tmem_st16(ts + 16 * c, y);
+                    }
+                    float a0, a1;
+                    split(add_pair(acc[0], acc[1]), a0, a1);
+                    l += a0 + a1;
+                    st_wait();
+                    fence_before();
+                    bar_arrive(p_full + 8 * q);
+                }
+                // ---- results
+                wait(o_done + 8 * q, (n_q + n_tiles - 1) & 1);
+                fence_after();
+                const float up = pow2f(ev);
+                const bool whole = s_seg.whole;
+                float *part = partials + ((long long)blockIdx.x * 2 + s_seg.begins) * partial_floats<D>();
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                uint16_t *dst = a.out + out_row * a.out_stride + (long long)head * D;
+#pragma unroll
+                for (int c = 0; c < D / 32; c++) {
+                    unsigned x[32];
+                    tmem_ld32(to + 32 * c, x);
+                    ld_wait();
+#pragma unroll
+                    for (int i = 0; i < 32; i++) x[i] = __float_as_uint(__uint_as_float(x[i]) * 128.0f * up);
+                    if (whole) {
+                        if (mine) {
+#pragma unroll
+                            for (int i = 0; i < 4; i++) {
+                                const int cb = (4 * c + i) / 8, chunk = (4 * c + i) % 8;
+                                const int d = (cb * M + chunk % M) * (D / 8) + 8 * (chunk / M);
+                                unsigned o4[4];
 #pragma unroll
                                 for (int e = 0; e < 4; e++) {
-                                    dst[d + 2 * e] = (uint16_t)o4[e];
-                                    dst[d + 2 * e + 1] = (uint16_t)(o4[e] >> 16);
+                                    // channels 2e, 2e + 1 of the eight; their columns are in the order 0 4 1 5 2 6 3 7
+                                    const int c0 = 2 * e < 4 ? 4 * e : 4 * (e - 2) + 1, c1 = 2 * e + 1 < 4 ? 4 * e + 2 : 4 * (e - 2) + 3;
+                                    float v0 = __uint_as_float(x[8 * i + c0]) * inv, v1 = __uint_as_float(x[8 * i + c1]) * inv;
+                                    if ((bits >> (d / G)) & 1u) v0 = v1 = __uint_as_float(0x7FC00000u);
+                                    o4[e] = float_to_bits<BF>(v0) | (float_to_bits<BF>(v1) << 16);
+                                }
+                                if (a.out_vec16) {
+                                    *reinterpret_cast<uint4 *>(dst + d) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+                                } else {
+#pragma unroll
+                                    for (int e = 0; e < 4; e++) {
+                                        dst[d + 2 * e] = (uint16_t)o4[e];
+                                        dst[d + 2 * e + 1] = (uint16_t)(o4[e] >> 16);
+                                    }
                                 }
                             }
                         }
-                    }
-                } else {
+                    } else {
 #pragma unroll
-                    for (int i = 0; i < 8; i++)
-                        *reinterpret_cast<uint4 *>(part + ((long long)(8 * c + i) * kRows + q * 128 + r) * 4) =
-                            make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                        for (int i = 0; i < 8; i++)
+                            *reinterpret_cast<uint4 *>(part + ((long long)(8 * c + i) * kRows + q * 128 + r) * 4) =
+                                make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
+                    }
                 }
+                if (whole) {
+                    if (mine && a.lse) a.lse[out_row * a.Hq + head] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * kLn2 + logf(l);
+                } else {
+                    float *tail = part + kRows * D + q * 128 + r;
+                    tail[0] = m;
+                    tail[kRows] = l;
+                    tail[2 * kRows] = __uint_as_float(bits);
+                }
+                fence_before();
+                n_q += n_tiles;
             }
-            if (g.whole) {
-                if (mine && a.lse)
-                    a.lse[(long long)(g.first + irow) * a.Hq + head] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * kLn2 + logf(l);
-            } else {
-                float *tail = part + kRows * D + q * 128 + r;
-                tail[0] = m;
-                tail[kRows] = l;
-                tail[2 * kRows] = __uint_as_float(bits);
-            }
-            fence_before();
-        }
-
-        // ---- an item of several CTAs: the last one joins
-        if (!g.whole) {
-            const long long c0 = cta_of(g.item_u0, total, grid), c1 = cta_of(g.item_u1 - 1, total, grid);
-            const int count = (int)(c1 - c0 + 1);
+            n_kv += n_tiles;
+            if (s_seg.whole) continue;
+            // ---- an item of several CTAs: the last one joins
             __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                const unsigned was = atomicAdd(tickets + c0, 1u);
-                s_last = was == (unsigned)(count - 1);
-                if (s_last) tickets[c0] = 0;
-            }
-            __syncthreads();
+            __syncthreads();  // (d)
+            __syncthreads();  // (e)
             if (s_last && mine) {
                 __threadfence();
+                const int count = s_seg.count, at = q * 128 + r;
+                const long long c0 = s_seg.cta0;
                 auto part_of = [&](int k) { return partials + ((c0 + k) * 2 + (k == 0 ? 1 : 0)) * partial_floats<D>(); };
-                const int at = q * 128 + r;
                 float top = -INFINITY;
                 for (int k = 0; k < count; k++) top = fmaxf(top, __ldcg(part_of(k) + kRows * D + at));
                 const float base = top == -INFINITY ? 0.0f : top;
@@ -846,7 +922,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                     bits |= __float_as_uint(__ldcg(tail + 2 * kRows));
                 }
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-                uint16_t *dst = a.out + (long long)(g.first + irow) * a.out_stride + (long long)head * D;
+                uint16_t *dst = a.out + out_row * a.out_stride + (long long)head * D;
+#pragma unroll 1
                 for (int c8 = 0; c8 < D / 8; c8++) {  // eight columns: eight channels
                     float x[8];
 #pragma unroll
@@ -859,7 +936,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                         x[0] += y.x * f, x[1] += y.y * f, x[2] += y.z * f, x[3] += y.w * f;
                         x[4] += z.x * f, x[5] += z.y * f, x[6] += z.z * f, x[7] += z.w * f;
                     }
-                    constexpr int M = 8 / NB;
                     const int cb = c8 / 8, chunk = c8 % 8, d = (cb * M + chunk % M) * (D / 8) + 8 * (chunk / M);
 #pragma unroll
                     for (int i = 0; i < 8; i++) {
@@ -867,16 +943,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                         dst[d + (i & 1 ? 4 + i / 2 : i / 2)] = (uint16_t)float_to_bits<BF>(v);
                     }
                 }
-                if (a.lse) a.lse[(long long)(g.first + irow) * a.Hq + head] = l == 0.0f ? -INFINITY : base * kLn2 + logf(l);
+                if (a.lse) a.lse[out_row * a.Hq + head] = l == 0.0f ? -INFINITY : base * kLn2 + logf(l);
             }
         }
-        n_kv += n_tiles;
-        n_q[0] += n_tiles;
-        if (nq == 2) n_q[1] += n_tiles;
-        u += n_tiles;
     }
     __syncthreads();
-    if (warp == 12) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+    if (warp == 16) asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
 }
 
 constexpr int kMaxGrid = 256;
