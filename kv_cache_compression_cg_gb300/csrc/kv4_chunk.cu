@@ -52,23 +52,46 @@ __device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
         : "memory");
     return ok != 0;
 }
+// Matrices in shared memory: rows (K-major) or tokens (MN-major) of 128 bytes in blocks of 8, 1024 bytes, swizzled by
+// 128 bytes; lead: bytes between 64-channel blocks along the contiguous side of an MN-major matrix.
+constexpr unsigned kHi128 = (1024 >> 4) | (1u << 14) | (2u << 29);
+__device__ __forceinline__ unsigned lo128(unsigned addr, unsigned lead) { return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16); }
+// 16 channels a row, without swizzle: blocks of 8 rows x 16 bytes, 128 bytes each; the two blocks of 8 channels
+// are 128 bytes apart, blocks of 8 rows 256.
+constexpr unsigned kHiNarrow = (256 >> 4) | (1u << 14);
+__device__ __forceinline__ unsigned lo_narrow(unsigned addr) { return lo128(addr, 128); }
 // Issued by the whole warp's one elected lane (issue != 0): control flow stays uniform, so operands stay in uniform registers.
 // The descriptors' upper word is the same for all matrices of a kind.
+// The steps' offsets are immediates: kept out of the compiler's sight, which would hold each sum in a register of its own.
+template <int kOffA, int kOffB>
 __device__ __forceinline__ void mma_ss(unsigned d, unsigned a, unsigned b, unsigned hi, unsigned idesc, bool add, unsigned issue) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
-        "mov.b64 x, {%1, %3};\n\tmov.b64 y, {%2, %3};\n\t"
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "add.u32 u, %1, %7;\n\tadd.u32 v, %2, %8;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
         "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((unsigned)add), "r"(issue)
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((unsigned)add), "r"(issue), "n"(kOffA), "n"(kOffB)
         : "memory");
 }
+template <int kOffA, int kOffB>
 __device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned b, unsigned hi, unsigned idesc, bool add, unsigned issue) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
-        "mov.b64 y, {%2, %3};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((unsigned)add), "r"(issue)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t.reg .b32 u, v;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
+        "add.u32 u, %1, %7;\n\tadd.u32 v, %2, %8;\n\tmov.b64 y, {v, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((unsigned)add), "r"(issue), "n"(kOffA), "n"(kOffB)
         : "memory");
+}
+// S = Q K' over D channels; O (+)= P V over 128 keys.
+template <int K, int D>
+__device__ __forceinline__ void mma_scores(unsigned d, unsigned a, unsigned b, unsigned idesc, unsigned issue) {
+    constexpr int off = ((K / 4) * 16384 + (K % 4) * 32) >> 4;
+    mma_ss<off, off>(d, a, b, kHi128, idesc, K > 0, issue);
+    if constexpr (K + 1 < D / 16) mma_scores<K + 1, D>(d, a, b, idesc, issue);
+}
+template <int K>
+__device__ __forceinline__ void mma_values(unsigned d, unsigned a, unsigned b, unsigned idesc, bool add, unsigned issue) {
+    mma_ts<8 * K, K * (2048 >> 4)>(d, a, b, kHi128, idesc, add || K > 0, issue);
+    if constexpr (K + 1 < kKT / 16) mma_values<K + 1>(d, a, b, idesc, add, issue);
 }
 __device__ __forceinline__ void mma_commit(unsigned bar, unsigned issue) {
     asm volatile(
@@ -134,14 +157,6 @@ __device__ __forceinline__ void tmem_st16(unsigned addr, const unsigned *r) {
         : "memory");
 }
 
-// Matrices in shared memory: rows (K-major) or tokens (MN-major) of 128 bytes in blocks of 8, 1024 bytes, swizzled by
-// 128 bytes; lead: bytes between 64-channel blocks along the contiguous side of an MN-major matrix.
-constexpr unsigned kHi128 = (1024 >> 4) | (1u << 14) | (2u << 29);
-__device__ __forceinline__ unsigned lo128(unsigned addr, unsigned lead) { return ((addr & 0x3FFFFu) >> 4) | ((lead >> 4) << 16); }
-// 16 channels a row, without swizzle: blocks of 8 rows x 16 bytes, 128 bytes each; the two blocks of 8 channels
-// are 128 bytes apart, blocks of 8 rows 256.
-constexpr unsigned kHiNarrow = (256 >> 4) | (1u << 14);
-__device__ __forceinline__ unsigned lo_narrow(unsigned addr) { return lo128(addr, 128); }
 // kind::f16, binary16 in, binary32 out, M = 128.
 __host__ __device__ constexpr unsigned idesc_f16(int n, bool b_mn) {
     return (1u << 4) | ((unsigned)b_mn << 16) | ((unsigned)(n >> 3) << 17) | (8u << 24);
@@ -312,7 +327,59 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     unsigned n_kv = 0;         // key tiles this CTA has begun: stage and parity of K, V
     unsigned n_q0 = 0, n_q1 = 0;  // tiles of S, P, O of either row tile
 
-    if (warp >= 16) {
+    if (warp == 16) {
+        regs_less<kRegsRest>();
+        // ---- matrix instructions
+        const unsigned issue = lane == 0;
+        for (;;) {
+            __syncthreads();  // (a)
+            __syncthreads();  // (b)
+            if (!s_seg.more) break;
+            const int n_tiles = s_seg.tiles, nq = s_seg.n * a.R - s_seg.row0 > 128 ? 2 : 1;
+            __syncthreads();  // (c)
+            constexpr unsigned id_s = idesc_f16(kKT, false), id_o = idesc_f16(D, true);
+            auto scores = [&](int i, unsigned kv) {
+                const unsigned st = kv & 1, d = tmem + kS0 + i * kKT;
+                const unsigned qa = lo128(smb + S::kQ + i * S::kQTile, 16), ka = lo128(smb + S::kK + st * S::kKStage, 16);
+                mma_scores<0, D>(d, qa, ka, id_s, issue);
+                mma_ss<0, 0>(d, lo_narrow(smb + S::kQN + i * 4096), lo_narrow(smb + S::kKN + st * 4096), kHiNarrow, id_s, true, issue);
+                mma_commit(s_full + 8 * i, issue);
+            };
+            unsigned kv = n_kv;
+            wait(k_full + 8 * (kv & 1), (kv >> 1) & 1);
+            fence_after();
+            for (int i = 0; i < nq; i++) scores(i, kv);
+            mma_commit(k_empty + 8 * (kv & 1), issue);
+            for (int j = 0; j < n_tiles; j++, kv++) {
+                wait(v_full + 8 * (kv & 1), (kv >> 1) & 1);
+                for (int i = 0; i < nq; i++) {
+                    wait(p_full + 8 * i, ((i ? n_q1 : n_q0) + j) & 1);
+                    fence_after();
+                    const unsigned st = kv & 1, d = tmem + kO0 + i * D, pa = tmem + kS0 + i * kKT;
+                    const unsigned va = lo128(smb + S::kV + st * S::kKStage, 16384);
+                    mma_values<0>(d, pa, va, id_o, j > 0, issue);
+                    mma_commit(o_done + 8 * i, issue);
+                    if (i == nq - 1) mma_commit(v_empty + 8 * st, issue);
+                    if (j + 1 < n_tiles) {
+                        if (i == 0) {
+                            wait(k_full + 8 * ((kv + 1) & 1), ((kv + 1) >> 1) & 1);
+                            fence_after();
+                        }
+                        scores(i, kv + 1);
+                        if (i == nq - 1) mma_commit(k_empty + 8 * ((kv + 1) & 1), issue);
+                    }
+                }
+            }
+            __syncwarp();
+            n_kv += n_tiles;
+            n_q0 += n_tiles;
+            if (nq == 2) n_q1 += n_tiles;
+            if (!s_seg.whole) {
+                __syncthreads();  // (d)
+                __syncthreads();  // (e)
+            }
+        }
+    } else if (warp > 16) {
         regs_less<kRegsRest>();
         const bool finder = warp == 17;
         long long u = total * blockIdx.x / grid;
@@ -339,7 +406,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                 before += __shfl_sync(0xFFFFFFFFu, incl, 31);
             }
         }
-        const unsigned issue = lane == 0;
         for (;;) {
             __syncthreads();  // (a)
             if (finder && lane == 0) {
@@ -383,56 +449,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             }
             __syncthreads();  // (b)
             if (!s_seg.more) break;
-            const int n_tiles = s_seg.tiles, nq = s_seg.n * a.R - s_seg.row0 > 128 ? 2 : 1;
             __syncthreads();  // (c)
-            if (warp == 16) {
-                // ---- matrix instructions
-                constexpr unsigned id_s = idesc_f16(kKT, false), id_o = idesc_f16(D, true);
-                auto scores = [&](int i, unsigned kv) {
-                    const unsigned st = kv & 1, d = tmem + kS0 + i * kKT;
-                    const unsigned qa = lo128(smb + S::kQ + i * S::kQTile, 16), ka = lo128(smb + S::kK + st * S::kKStage, 16);
-#pragma unroll
-                    for (int k = 0; k < D / 16; k++) {
-                        const unsigned off = ((k / 4) * 16384 + (k % 4) * 32) >> 4;
-                        mma_ss(d, qa + off, ka + off, kHi128, id_s, k > 0, issue);
-                    }
-                    mma_ss(d, lo_narrow(smb + S::kQN + i * 4096), lo_narrow(smb + S::kKN + st * 4096), kHiNarrow, id_s, true, issue);
-                    mma_commit(s_full + 8 * i, issue);
-                };
-                unsigned kv = n_kv;
-                wait(k_full + 8 * (kv & 1), (kv >> 1) & 1);
-                fence_after();
-                for (int i = 0; i < nq; i++) scores(i, kv);
-                mma_commit(k_empty + 8 * (kv & 1), issue);
-                for (int j = 0; j < n_tiles; j++, kv++) {
-                    wait(v_full + 8 * (kv & 1), (kv >> 1) & 1);
-                    for (int i = 0; i < nq; i++) {
-                        wait(p_full + 8 * i, ((i ? n_q1 : n_q0) + j) & 1);
-                        fence_after();
-                        const unsigned st = kv & 1, d = tmem + kO0 + i * D, pa = tmem + kS0 + i * kKT;
-                        const unsigned va = lo128(smb + S::kV + st * S::kKStage, 16384);
-#pragma unroll
-                        for (int k = 0; k < kKT / 16; k++)
-                            mma_ts(d, pa + 8 * k, va + k * (2048 >> 4), kHi128, id_o, j > 0 || k > 0, issue);
-                        mma_commit(o_done + 8 * i, issue);
-                        if (i == nq - 1) mma_commit(v_empty + 8 * st, issue);
-                        if (j + 1 < n_tiles) {
-                            if (i == 0) {
-                                wait(k_full + 8 * ((kv + 1) & 1), ((kv + 1) >> 1) & 1);
-                                fence_after();
-                            }
-                            scores(i, kv + 1);
-                            if (i == nq - 1) mma_commit(k_empty + 8 * ((kv + 1) & 1), issue);
-                        }
-                    }
-                }
-                __syncwarp();
-            }
-            const bool whole = s_seg.whole;
-            n_kv += n_tiles;
-            n_q0 += n_tiles;
-            if (nq == 2) n_q1 += n_tiles;
-            if (!whole) {
+            if (!s_seg.whole) {
                 __syncthreads();  // (d)
                 if (finder && lane == 0) {
                     unsigned *tickets = static_cast<unsigned *>(a.ws);
