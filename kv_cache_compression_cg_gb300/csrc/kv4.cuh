@@ -135,7 +135,7 @@ struct Kv4Attend {
     void *ws;                 // tickets (ticket_bytes, zero between calls), then partial results
     long long ticket_bytes;
     bool q_vec, out_vec;      // rows allow 8-byte loads, stores
-    bool out_vec16;           // and 16-byte stores
+    bool q_vec16, out_vec16;  // and 16-byte loads, stores
     int step_max;             // (rows x R) of a sequence up to which it is the step kernel's,
     int chunk_min;            // from which on the chunk kernel's
 };

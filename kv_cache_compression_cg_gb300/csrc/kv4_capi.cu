@@ -170,6 +170,7 @@ cg_status cg_kv4_attention(const uint8_t *pool, const cg_kv4_shape *shape, const
     a.ticket_bytes = (long long)cg::kv4_ticket_bytes();
     a.q_vec = aligned(q, 8) && q_row_stride % 4 == 0;
     a.out_vec = aligned(out, 8) && out_row_stride % 4 == 0;
+    a.q_vec16 = aligned(q, 16) && q_row_stride % 8 == 0;
     a.out_vec16 = aligned(out, 16) && out_row_stride % 8 == 0;
     const Plan plan = plan_of(p, a.R);
     a.step_max = plan.chunk ? kStepCols : 0x7FFFFFFF;

@@ -233,14 +233,36 @@ __device__ __forceinline__ void tiles_of(const Span &s, const Kv4Attend &a, int 
         tiles = (int)((end + kKT - 1) / kKT) - t0;
     }
 }
-__device__ __forceinline__ long long units_of(const Kv4 &p, const Kv4Attend &a, int b, int32_t *status) {
-    const Span s = span_of(p, a, b, status);
+// Units (key tiles of all pairs, over the KV heads) of sequence b0 + lane. Called by a whole warp; sequences of many
+// pairs are summed by all lanes together.
+__device__ __forceinline__ long long units_of_group(const Kv4 &p, const Kv4Attend &a, int b0, int lane, int32_t *status) {
+    Span s{0, 0, 0, 0};
+    if (b0 + lane < p.B) s = span_of(p, a, b0 + lane, status);
     const int pairs = (s.n * a.R + kRows - 1) / kRows;
     long long sum = 0;
-    for (int i = 0; i < pairs; i++) {
-        int t0, tiles;
-        tiles_of(s, a, i, t0, tiles);
-        sum += tiles;
+    int t0, tiles;
+    if (__all_sync(0xFFFFFFFFu, pairs <= 4)) {
+        for (int i = 0; i < pairs; i++) {
+            tiles_of(s, a, i, t0, tiles);
+            sum += tiles;
+        }
+    } else {
+        for (unsigned todo = __ballot_sync(0xFFFFFFFFu, pairs > 0); todo; todo &= todo - 1) {
+            const int src = __ffs(todo) - 1;
+            Span o;
+            o.first = 0;
+            o.n = __shfl_sync(0xFFFFFFFFu, s.n, src);
+            o.len = __shfl_sync(0xFFFFFFFFu, s.len, src);
+            o.pos0 = __shfl_sync(0xFFFFFFFFu, s.pos0, src);
+            const int many = __shfl_sync(0xFFFFFFFFu, pairs, src);
+            int mine = 0;
+            for (int i = lane; i < many; i += 32) {
+                tiles_of(o, a, i, t0, tiles);
+                mine += tiles;
+            }
+            mine = __reduce_add_sync(0xFFFFFFFFu, mine);
+            if (lane == src) sum = mine;
+        }
     }
     return sum * p.H;
 }
@@ -268,10 +290,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     __shared__ Info s_info[4];
     __shared__ uint8_t s_odd[4][kKT];  // bits of a token's value groups that are not finite
     __shared__ float s_emax[2][2][8];
-    __shared__ Segment s_seg;
+    __shared__ Segment s_segs[2];
     __shared__ long long s_sum[kThreads / 32];
 
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // the shuffle: known to be uniform
     uint8_t *sm = raw + ((1024 - (saddr(raw) & 1023)) & 1023);
     const unsigned smb = saddr(sm);
     const unsigned bb = saddr(bars);
@@ -280,7 +302,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
 
     // ---- how much work there is
     long long sum = 0;
-    for (int b = threadIdx.x; b < p.B; b += kThreads) sum += units_of(p, a, b, a.status);
+    for (int b0 = warp * 32; b0 < p.B; b0 += kThreads) sum += units_of_group(p, a, b0, lane, a.status);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) s_sum[warp] = sum;
@@ -298,10 +320,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
-    long long total = 0;
-    for (int i = 0; i < kThreads / 32; i++) total += s_sum[i];
-    const long long grid = total < gridDim.x ? total : gridDim.x;
-    if (blockIdx.x >= grid) return;
     if (warp == 16) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(saddr(&s_tmem)) : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
@@ -309,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     }
     __syncthreads();
     fence_after();
-    const unsigned tmem = s_tmem;
+    const unsigned tmem = __shfl_sync(0xFFFFFFFFu, s_tmem, 0);
 
     // Waits are bounded: the first to run out stops all others, and the call reports CG_FLAG_TIMEOUT.
     auto wait = [&](unsigned bar, unsigned parity) {
@@ -322,7 +340,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             }
         }
     };
-    // Each role runs the same rounds, one a segment: (a) the last one is over, (b) its description is there, (c) its queries
+    // Each role runs the same rounds, one a segment: (b) its description is there and the last one is over, (c) its queries
     // are in place, then where an item is shared (d) partial results are out, (e) the ticket is drawn.
     unsigned n_kv = 0;         // key tiles this CTA has begun: stage and parity of K, V
     unsigned n_q0 = 0, n_q1 = 0;  // tiles of S, P, O of either row tile
@@ -331,11 +349,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
         regs_less<kRegsRest>();
         // ---- matrix instructions
         const unsigned issue = lane == 0;
-        for (;;) {
-            __syncthreads();  // (a)
+        for (unsigned round = 0;; round++) {
             __syncthreads();  // (b)
+            const Segment &s_seg = s_segs[round & 1];
             if (!s_seg.more) break;
-            const int n_tiles = s_seg.tiles, nq = s_seg.n * a.R - s_seg.row0 > 128 ? 2 : 1;
+            const int n_tiles = __shfl_sync(0xFFFFFFFFu, s_seg.tiles, 0);
+            const bool two = __shfl_sync(0xFFFFFFFFu, s_seg.n * a.R - s_seg.row0 > 128, 0);
             __syncthreads();  // (c)
             constexpr unsigned id_s = idesc_f16(kKT, false), id_o = idesc_f16(D, true);
             auto scores = [&](int i, unsigned kv) {
@@ -348,32 +367,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             unsigned kv = n_kv;
             wait(k_full + 8 * (kv & 1), (kv >> 1) & 1);
             fence_after();
-            for (int i = 0; i < nq; i++) scores(i, kv);
+            scores(0, kv);
+            if (two) scores(1, kv);
             mma_commit(k_empty + 8 * (kv & 1), issue);
+            auto turn = [&](int i, int j, unsigned parity, bool last) {
+                wait(p_full + 8 * i, parity);
+                fence_after();
+                const unsigned st = kv & 1;
+                mma_values<0>(tmem + kO0 + i * D, tmem + kS0 + i * kKT, lo128(smb + S::kV + st * S::kKStage, 16384), id_o, j > 0, issue);
+                mma_commit(o_done + 8 * i, issue);
+                if (last) mma_commit(v_empty + 8 * st, issue);
+                if (j + 1 < n_tiles) {
+                    if (i == 0) {
+                        wait(k_full + 8 * (st ^ 1), ((kv + 1) >> 1) & 1);
+                        fence_after();
+                    }
+                    scores(i, kv + 1);
+                    if (last) mma_commit(k_empty + 8 * (st ^ 1), issue);
+                }
+            };
             for (int j = 0; j < n_tiles; j++, kv++) {
                 wait(v_full + 8 * (kv & 1), (kv >> 1) & 1);
-                for (int i = 0; i < nq; i++) {
-                    wait(p_full + 8 * i, ((i ? n_q1 : n_q0) + j) & 1);
-                    fence_after();
-                    const unsigned st = kv & 1, d = tmem + kO0 + i * D, pa = tmem + kS0 + i * kKT;
-                    const unsigned va = lo128(smb + S::kV + st * S::kKStage, 16384);
-                    mma_values<0>(d, pa, va, id_o, j > 0, issue);
-                    mma_commit(o_done + 8 * i, issue);
-                    if (i == nq - 1) mma_commit(v_empty + 8 * st, issue);
-                    if (j + 1 < n_tiles) {
-                        if (i == 0) {
-                            wait(k_full + 8 * ((kv + 1) & 1), ((kv + 1) >> 1) & 1);
-                            fence_after();
-                        }
-                        scores(i, kv + 1);
-                        if (i == nq - 1) mma_commit(k_empty + 8 * ((kv + 1) & 1), issue);
-                    }
-                }
+                turn(0, j, (n_q0 + j) & 1, !two);
+                if (two) turn(1, j, (n_q1 + j) & 1, true);
             }
             __syncwarp();
             n_kv += n_tiles;
             n_q0 += n_tiles;
-            if (nq == 2) n_q1 += n_tiles;
+            if (two) n_q1 += n_tiles;
             if (!s_seg.whole) {
                 __syncthreads();  // (d)
                 __syncthreads();  // (e)
@@ -382,74 +403,93 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     } else if (warp > 16) {
         regs_less<kRegsRest>();
         const bool finder = warp == 17;
-        long long u = total * blockIdx.x / grid;
-        const long long u_end = total * (blockIdx.x + 1) / grid;
-        int cur_b = 0;
-        long long before = 0, all = 0;  // units of the sequences before cur_b, and of cur_b
-        if (finder) {
-            for (int b0 = 0; b0 < p.B; b0 += 32) {
-                const long long x = b0 + lane < p.B ? units_of(p, a, b0 + lane, nullptr) : 0;
-                long long incl = x;
+        long long total = 0;
+        for (int i = 0; i < kThreads / 32; i++) total += s_sum[i];
+        const long long grid = total < gridDim.x ? total : gridDim.x;  // CTAs that get work
+        const bool idle = blockIdx.x >= grid;
+        long long u = idle ? 0 : total * blockIdx.x / grid;
+        const long long u_end = idle ? 0 : total * (blockIdx.x + 1) / grid;
+        int b0 = 0, cur = 0;                     // sequences b0.. of this group, the one in work
+        long long before = 0, x = 0, incl = 0;   // units before the group; of each lane's sequence; up to its end
+        auto group = [&]() {
+            x = units_of_group(p, a, b0, lane, nullptr);
+            incl = x;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+                if (lane >= o) incl += y;
+            }
+        };
+        // The description of the segment that begins at u, by the whole warp.
+        auto find = [&](Segment &g) {
+            if (lane == 0) g.more = u < u_end;
+            if (u >= u_end) return;
+            unsigned hit;
+            while (!(hit = __ballot_sync(0xFFFFFFFFu, before + incl > u))) {
+                before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+                b0 += 32;
+                group();
+            }
+            cur = __ffs(hit) - 1;
+            const long long all = __shfl_sync(0xFFFFFFFFu, x, cur), begin = before + __shfl_sync(0xFFFFFFFFu, incl - x, cur);
+            const Span s = span_of(p, a, b0 + cur, nullptr);
+            const long long per = all / p.H;
+            int rest = (int)((u - begin) % per);
+            int t0 = 0, tiles = 0, pair = 0;
+            for (;; pair += 32) {  // 32 pairs at a time
+                const int pairs = (s.n * a.R + kRows - 1) / kRows;
+                int mine = 0, from = 0;
+                if (pair + lane < pairs) tiles_of(s, a, pair + lane, from, mine);
+                int upto = mine;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
-                    const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                    if (lane >= o) incl += y;
+                    const int y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
+                    if (lane >= o) upto += y;
                 }
-                const unsigned hit = __ballot_sync(0xFFFFFFFFu, before + incl > u);
-                if (hit) {
-                    const int src = __ffs(hit) - 1;
-                    cur_b = b0 + src;
-                    before += __shfl_sync(0xFFFFFFFFu, incl - x, src);
-                    all = __shfl_sync(0xFFFFFFFFu, x, src);
+                const unsigned at = __ballot_sync(0xFFFFFFFFu, upto > rest);
+                if (at) {
+                    const int src = __ffs(at) - 1;
+                    rest -= __shfl_sync(0xFFFFFFFFu, upto - mine, src);
+                    t0 = __shfl_sync(0xFFFFFFFFu, from, src);
+                    tiles = __shfl_sync(0xFFFFFFFFu, mine, src);
+                    pair += src;
                     break;
                 }
-                before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+                rest -= __shfl_sync(0xFFFFFFFFu, upto, 31);
             }
-        }
-        for (;;) {
-            __syncthreads();  // (a)
-            if (finder && lane == 0) {
-                s_seg.more = u < u_end;
-                if (u < u_end) {
-                    while (u - before >= all) {
-                        before += all;
-                        cur_b++;
-                        all = units_of(p, a, cur_b, nullptr);
-                    }
-                    const Span s = span_of(p, a, cur_b, nullptr);
-                    const long long per = all / p.H;
-                    long long rest = (u - before) % per;
-                    int pair = 0, t0, tiles;
-                    tiles_of(s, a, 0, t0, tiles);
-                    while (rest >= tiles) {
-                        rest -= tiles;
-                        tiles_of(s, a, ++pair, t0, tiles);
-                    }
-                    const long long left = u_end - u;
-                    const int here = left < tiles - rest ? (int)left : (int)(tiles - rest);
-                    s_seg.b = cur_b;
-                    s_seg.kvh = (int)((u - before) / per);
-                    s_seg.row0 = pair * kRows;
-                    s_seg.first = s.first;
-                    s_seg.n = s.n;
-                    s_seg.len = s.len;
-                    s_seg.pos0 = s.pos0;
-                    s_seg.tile0 = t0 + (int)rest;
-                    s_seg.tiles = here;
-                    s_seg.begins = rest == 0;
-                    s_seg.whole = here == tiles;
-                    s_seg.cta0 = 0;
-                    s_seg.count = 1;
-                    if (here != tiles) {
-                        s_seg.cta0 = (int)cta_of(u - rest, total, grid);
-                        s_seg.count = (int)cta_of(u - rest + tiles - 1, total, grid) - s_seg.cta0 + 1;
-                    }
-                    u += here;
+            const long long left = u_end - u;
+            const int here = left < tiles - rest ? (int)left : tiles - rest;
+            if (lane == 0) {
+                g.b = b0 + cur;
+                g.kvh = (int)((u - begin) / per);
+                g.row0 = pair * kRows;
+                g.first = s.first;
+                g.n = s.n;
+                g.len = s.len;
+                g.pos0 = s.pos0;
+                g.tile0 = t0 + rest;
+                g.tiles = here;
+                g.begins = rest == 0;
+                g.whole = here == tiles;
+                g.cta0 = 0;
+                g.count = 1;
+                if (here != tiles) {
+                    g.cta0 = (int)cta_of(u - rest, total, grid);
+                    g.count = (int)cta_of(u - rest + tiles - 1, total, grid) - g.cta0 + 1;
                 }
             }
+            u += here;
+        };
+        if (finder) {
+            group();
+            find(s_segs[0]);
+        }
+        for (unsigned round = 0;; round++) {
             __syncthreads();  // (b)
+            const Segment &s_seg = s_segs[round & 1];
             if (!s_seg.more) break;
             __syncthreads();  // (c)
+            if (finder) find(s_segs[(round + 1) & 1]);  // while this one is in work
             if (!s_seg.whole) {
                 __syncthreads();  // (d)
                 if (finder && lane == 0) {
@@ -467,9 +507,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
         // ---- K and V of the tiles: warp w has record w of each; lanes as in the step kernel
         const int w = warp - 8, gl = lane >> 2, t = lane & 3, gv = gl * (D / 8) / G;
         const int rpp = p.P / kBlk;
-        for (;;) {
-            __syncthreads();  // (a)
+        for (unsigned round = 0;; round++) {
             __syncthreads();  // (b)
+            const Segment &s_seg = s_segs[round & 1];
             if (!s_seg.more) break;
             const int tile0 = s_seg.tile0, n_tiles = s_seg.tiles, len = s_seg.len;
             const int *table = p.table + (long long)s_seg.b * p.max_pages;
@@ -696,9 +736,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
         const unsigned ts = tmem + kS0 + q * kKT + ((unsigned)(warp & 3) << 21), to = tmem + kO0 + q * D + ((unsigned)(warp & 3) << 21);
         float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + a.ticket_bytes);
         unsigned n_q = 0;
-        for (;;) {
-            __syncthreads();  // (a)
+        for (unsigned round = 0;; round++) {
             __syncthreads();  // (b)
+            const Segment &s_seg = s_segs[round & 1];
             if (!s_seg.more) break;
             const int tile0 = s_seg.tile0, n_tiles = s_seg.tiles, len = s_seg.len;
             const int rho = s_seg.row0 + q * 128 + r;
@@ -710,26 +750,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             // 16 more on, w = 2 block + chunk % 2, t = chunk / 2: the order K's chunks come in
             {
                 const uint16_t *src = a.q + out_row * a.q_stride + (long long)head * D;
-                auto four = [&](int d, unsigned &x, unsigned &y) {
-                    x = y = 0;
-                    if (!mine) return;
-                    if (a.q_vec) {
-                        const uint2 w = *reinterpret_cast<const uint2 *>(src + d);
-                        x = w.x;
-                        y = w.y;
-                    } else {
-                        x = src[d] | ((unsigned)src[d + 1] << 16);
-                        y = src[d + 2] | ((unsigned)src[d + 3] << 16);
+                unsigned in[D / 2];  // pairs of channels
+                if (!mine) {
+#pragma unroll
+                    for (int d = 0; d < D / 2; d++) in[d] = 0;
+                } else if (a.q_vec16) {
+#pragma unroll
+                    for (int d = 0; d < D / 8; d++) {
+                        const uint4 w = __ldg(reinterpret_cast<const uint4 *>(src) + d);
+                        in[4 * d] = w.x, in[4 * d + 1] = w.y, in[4 * d + 2] = w.z, in[4 * d + 3] = w.w;
                     }
-                };
-                float top = 0.0f;
-#pragma unroll 8
-                for (int d = 0; d < D; d += 4) {
-                    unsigned x, y;
-                    four(d, x, y);
-                    top = fmaxf(top, fmaxf(fmaxf(fabsf(bits_to_float<BF>(x & 0xFFFFu)), fabsf(bits_to_float<BF>(x >> 16))),
-                                           fmaxf(fabsf(bits_to_float<BF>(y & 0xFFFFu)), fabsf(bits_to_float<BF>(y >> 16)))));
+                } else {
+#pragma unroll
+                    for (int d = 0; d < D / 2; d++) in[d] = src[2 * d] | ((unsigned)src[2 * d + 1] << 16);
                 }
+                float top = 0.0f;
+#pragma unroll
+                for (int d = 0; d < D / 2; d++) top = max3(top, fabsf(bits_to_float<BF>(in[d] & 0xFFFFu)), fabsf(bits_to_float<BF>(in[d] >> 16)));
                 // the row's largest goes to [2^7, 2^8): sums over a group stay below 2^15
                 int kq = top > 0.0f ? 7 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
                 kq = kq > 120 ? 120 : kq;
@@ -742,9 +779,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
 #pragma unroll
                 for (int c = 0; c < D / 8; c++) {
                     const int block = c / 8, chunk = c % 8, w = 2 * block + (chunk & 1), t = chunk >> 1;
-                    unsigned x[4];
-                    four(32 * w + 4 * t, x[0], x[1]);
-                    four(32 * w + 16 + 4 * t, x[2], x[3]);
+                    const int d0 = 16 * w + 2 * t;
+                    unsigned x[4] = {in[d0], in[d0 + 1], in[d0 + 8], in[d0 + 9]};
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
                         x[i] = pack_half(bits_to_float<BF>(x[i] & 0xFFFFu) * f, bits_to_float<BF>(x[i] >> 16) * f);
@@ -941,7 +977,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                 }
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 uint16_t *dst = a.out + out_row * a.out_stride + (long long)head * D;
-#pragma unroll 1
+#pragma unroll 4
                 for (int c8 = 0; c8 < D / 8; c8++) {  // eight columns: eight channels
                     float x[8];
 #pragma unroll
