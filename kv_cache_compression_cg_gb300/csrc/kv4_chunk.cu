@@ -60,44 +60,47 @@ __device__ __forceinline__ unsigned lo128(unsigned addr, unsigned lead) { return
 // are 128 bytes apart, blocks of 8 rows 256.
 constexpr unsigned kHiNarrow = (256 >> 4) | (1u << 14);
 __device__ __forceinline__ unsigned lo_narrow(unsigned addr) { return lo128(addr, 128); }
-// Issued by the whole warp's one elected lane (issue != 0): control flow stays uniform, so operands stay in uniform registers.
-// The descriptors' upper word is the same for all matrices of a kind.
+// One lane of a converged warp. (elect.sync, not a test of the lane's number: the compiler then knows that one thread
+// runs what follows, and the matrix instructions' operands go to uniform registers directly.)
+__device__ __forceinline__ bool elected() {
+    unsigned y;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(y));
+    return y != 0;
+}
 // The steps' offsets are immediates: kept out of the compiler's sight, which would hold each sum in a register of its own.
+// The descriptors' upper word is the same for all matrices of a kind.
 template <int kOffA, int kOffB>
-__device__ __forceinline__ void mma_ss(unsigned d, unsigned a, unsigned b, unsigned hi, unsigned idesc, bool add, unsigned issue) {
+__device__ __forceinline__ void mma_ss(unsigned d, unsigned a, unsigned b, unsigned hi, unsigned idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
-        "add.u32 u, %1, %7;\n\tadd.u32 v, %2, %8;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((unsigned)add), "r"(issue), "n"(kOffA), "n"(kOffB)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t.reg .b32 u, v;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "add.u32 u, %1, %6;\n\tadd.u32 v, %2, %7;\n\tmov.b64 x, {u, %3};\n\tmov.b64 y, {v, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((unsigned)add), "n"(kOffA), "n"(kOffB)
         : "memory");
 }
 template <int kOffA, int kOffB>
-__device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned b, unsigned hi, unsigned idesc, bool add, unsigned issue) {
+__device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned b, unsigned hi, unsigned idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\t.reg .b32 u, v;\n\tsetp.ne.u32 p, %5, 0;\n\tsetp.ne.u32 q, %6, 0;\n\t"
-        "add.u32 u, %1, %7;\n\tadd.u32 v, %2, %8;\n\tmov.b64 y, {v, %3};\n\t"
-        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p;\n\t}" ::"r"(d),
-        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((unsigned)add), "r"(issue), "n"(kOffA), "n"(kOffB)
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t.reg .b32 u, v;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+        "add.u32 u, %1, %6;\n\tadd.u32 v, %2, %7;\n\tmov.b64 y, {v, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [u], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((unsigned)add), "n"(kOffA), "n"(kOffB)
         : "memory");
 }
 // S = Q K' over D channels; O (+)= P V over 128 keys.
 template <int K, int D>
-__device__ __forceinline__ void mma_scores(unsigned d, unsigned a, unsigned b, unsigned idesc, unsigned issue) {
+__device__ __forceinline__ void mma_scores(unsigned d, unsigned a, unsigned b, unsigned idesc) {
     constexpr int off = ((K / 4) * 16384 + (K % 4) * 32) >> 4;
-    mma_ss<off, off>(d, a, b, kHi128, idesc, K > 0, issue);
-    if constexpr (K + 1 < D / 16) mma_scores<K + 1, D>(d, a, b, idesc, issue);
+    mma_ss<off, off>(d, a, b, kHi128, idesc, K > 0);
+    if constexpr (K + 1 < D / 16) mma_scores<K + 1, D>(d, a, b, idesc);
 }
 template <int K>
-__device__ __forceinline__ void mma_values(unsigned d, unsigned a, unsigned b, unsigned idesc, bool add, unsigned issue) {
-    mma_ts<8 * K, K * (2048 >> 4)>(d, a, b, kHi128, idesc, add || K > 0, issue);
-    if constexpr (K + 1 < kKT / 16) mma_values<K + 1>(d, a, b, idesc, add, issue);
+__device__ __forceinline__ void mma_values(unsigned d, unsigned a, unsigned b, unsigned idesc, bool add) {
+    mma_ts<8 * K, K * (2048 >> 4)>(d, a, b, kHi128, idesc, add || K > 0);
+    if constexpr (K + 1 < kKT / 16) mma_values<K + 1>(d, a, b, idesc, add);
 }
-__device__ __forceinline__ void mma_commit(unsigned bar, unsigned issue) {
-    asm volatile(
-        "{\n\t.reg .pred q;\n\tsetp.ne.u32 q, %1, 0;\n\t"
-        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(bar), "r"(issue)
-        : "memory");
+__device__ __forceinline__ void mma_commit(unsigned bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 template <int N>
 __device__ __forceinline__ void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -348,7 +351,6 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     if (warp == 16) {
         regs_less<kRegsRest>();
         // ---- matrix instructions
-        const unsigned issue = lane == 0;
         for (unsigned round = 0;; round++) {
             __syncthreads();  // (b)
             const Segment &s_seg = s_segs[round & 1];
@@ -360,30 +362,39 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             auto scores = [&](int i, unsigned kv) {
                 const unsigned st = kv & 1, d = tmem + kS0 + i * kKT;
                 const unsigned qa = lo128(smb + S::kQ + i * S::kQTile, 16), ka = lo128(smb + S::kK + st * S::kKStage, 16);
-                mma_scores<0, D>(d, qa, ka, id_s, issue);
-                mma_ss<0, 0>(d, lo_narrow(smb + S::kQN + i * 4096), lo_narrow(smb + S::kKN + st * 4096), kHiNarrow, id_s, true, issue);
-                mma_commit(s_full + 8 * i, issue);
+                mma_scores<0, D>(d, qa, ka, id_s);
+                mma_ss<0, 0>(d, lo_narrow(smb + S::kQN + i * 4096), lo_narrow(smb + S::kKN + st * 4096), kHiNarrow, id_s, true);
+                mma_commit(s_full + 8 * i);
             };
             unsigned kv = n_kv;
             wait(k_full + 8 * (kv & 1), (kv >> 1) & 1);
             fence_after();
-            scores(0, kv);
-            if (two) scores(1, kv);
-            mma_commit(k_empty + 8 * (kv & 1), issue);
+            if (elected()) {
+                scores(0, kv);
+                if (two) scores(1, kv);
+                mma_commit(k_empty + 8 * (kv & 1));
+            }
+            __syncwarp();
             auto turn = [&](int i, int j, unsigned parity, bool last) {
                 wait(p_full + 8 * i, parity);
                 fence_after();
                 const unsigned st = kv & 1;
-                mma_values<0>(tmem + kO0 + i * D, tmem + kS0 + i * kKT, lo128(smb + S::kV + st * S::kKStage, 16384), id_o, j > 0, issue);
-                mma_commit(o_done + 8 * i, issue);
-                if (last) mma_commit(v_empty + 8 * st, issue);
+                if (elected()) {
+                    mma_values<0>(tmem + kO0 + i * D, tmem + kS0 + i * kKT, lo128(smb + S::kV + st * S::kKStage, 16384), id_o, j > 0);
+                    mma_commit(o_done + 8 * i);
+                    if (last) mma_commit(v_empty + 8 * st);
+                }
+                __syncwarp();
                 if (j + 1 < n_tiles) {
                     if (i == 0) {
                         wait(k_full + 8 * (st ^ 1), ((kv + 1) >> 1) & 1);
                         fence_after();
                     }
-                    scores(i, kv + 1);
-                    if (last) mma_commit(k_empty + 8 * (st ^ 1), issue);
+                    if (elected()) {
+                        scores(i, kv + 1);
+                        if (last) mma_commit(k_empty + 8 * (st ^ 1));
+                    }
+                    __syncwarp();
                 }
             };
             for (int j = 0; j < n_tiles; j++, kv++) {
