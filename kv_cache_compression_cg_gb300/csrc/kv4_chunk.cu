@@ -837,7 +837,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                     const volatile Info *info = &s_info[kv & 3];
                     const int tok = (tile0 + j) * kKT, evj = info->ev;
                     const unsigned valid = info->valid;
-                    const float f = factor * pow2f(info->ek);
+                    const float f = fmaxf(factor * pow2f(info->ek), 1e-37f);  // never zero: a hidden score's -inf stays -inf
                     const bool plain = valid == 0xFFu && tok >= lo_w && tok + kKT - 1 <= hi_w;
                     ld_wait();
                     if (!plain) {

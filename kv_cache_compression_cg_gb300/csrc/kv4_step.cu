@@ -24,6 +24,7 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 32;              // tokens a warp takes at a time: two records
+constexpr int kJoin = 8;
 constexpr int kUnit = kTile * kWarps;  // tokens the work is dealt out in
 constexpr int kSigMin = -110;            // values below 2^-115 or so lose bits
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
@@ -53,6 +54,16 @@ __device__ __forceinline__ unsigned pack_half(float lo, float hi) {
 __device__ __forceinline__ unsigned fma_half(unsigned a, unsigned b, unsigned c) {
     unsigned y;
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
+    return y;
+}
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float y;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ unsigned mul_half(unsigned a, unsigned b) {
+    unsigned y;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
     return y;
 }
 __device__ __forceinline__ float exp2_approx(float x) {
@@ -124,11 +135,15 @@ __device__ __forceinline__ void put_out(const Kv4Attend &a, const Seq &s, int kv
         a.lse[(long long)row * a.Hq + h] = tl == 0.0f ? -INFINITY : (top == -INFINITY ? 0.0f : top) * kLn2 + logf(tl);
 }
 
+// a / b; most calls' numbers fit 32 bits, whose division is several times shorter.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
 // The CTA whose range [total * c / grid, total * (c + 1) / grid) has unit u.
 __device__ __forceinline__ long long cta_of(long long u, long long total, long long grid) {
-    long long c = u * grid / total;
-    while (total * c / grid > u) c--;
-    while (total * (c + 1) / grid <= u) c++;
+    long long c = quotient(u * grid, total);
+    while (total * c >= (u + 1) * grid) c--;        // floor(total c / grid) > u
+    while (total * (c + 1) < (u + 1) * grid) c++;   // floor(total (c + 1) / grid) <= u
     return c;
 }
 
@@ -138,64 +153,55 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
     constexpr int NG = R::NG, COLS = 8 * NT, ST = stages<D>(), KS = D / 16, W = D / 32;
     constexpr int RB = R::kBytes, TB = 2 * RB;
     extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ long long s_base[kWarps];
-    __shared__ long long s_mine;
-    __shared__ int s_b;
     __shared__ int s_last;
     __shared__ float s_m[kWarps][COLS], s_l[kWarps][COLS], s_sigma[kWarps];
     __shared__ unsigned s_bits[kWarps][COLS];
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
 
-    // ---- the total of all sequences' units, then the sequence that this CTA's range starts in
-    long long sum = 0;
-    for (int b = threadIdx.x; b < p.B; b += kThreads) {
-        const Seq s = seq_of(p, a, b, COLS, a.status);
-        sum += (long long)s.units * s.tiles * p.H;
-    }
+    // ---- the total of all sequences' units, then the sequence that this CTA's range starts in: by every warp for itself,
+    // 32 sequences at a time (a barrier would cost more than the repeated loads)
+    auto units = [&](int b0, int32_t *status) -> long long {
+        if (b0 + lane >= p.B) return 0;
+        const Seq s = seq_of(p, a, b0 + lane, COLS, status);
+        return (long long)s.units * s.tiles * p.H;
+    };
+    auto upto = [&](long long x) {
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) s_base[warp] = sum;
-    __syncthreads();
-    const long long total = s_base[0] + s_base[1] + s_base[2] + s_base[3];
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xFFFFFFFFu, x, o);
+            if (lane >= o) x += y;
+        }
+        return x;
+    };
+    const long long x0 = units(0, a.status), incl0 = upto(x0);
+    long long total = __shfl_sync(0xFFFFFFFFu, incl0, 31);
+    if (p.B > 32) {
+        long long more = 0;
+        for (int b0 = 32; b0 < p.B; b0 += 32) more += units(b0, a.status);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) more += __shfl_xor_sync(0xFFFFFFFFu, more, o);
+        total += more;
+    }
     const long long grid = total < gridDim.x ? total : gridDim.x;
     if (blockIdx.x >= grid) return;
-    long long u = total * blockIdx.x / grid;
-    const long long u_end = total * (blockIdx.x + 1) / grid;
+    long long u = quotient(total * blockIdx.x, grid);
+    const long long u_end = quotient(total * (blockIdx.x + 1), grid);
     int b = 0;
     long long before = 0;  // units of the sequences before b
-    if (warp == 0) {
-        long long base = 0;
-        int at = 0;
-        for (int b0 = 0; b0 < p.B; b0 += 32) {
-            long long x = 0;
-            if (b0 + lane < p.B) {
-                const Seq s = seq_of(p, a, b0 + lane, COLS, nullptr);
-                x = (long long)s.units * s.tiles * p.H;
-            }
-            long long incl = x;
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const long long y = __shfl_up_sync(0xFFFFFFFFu, incl, o);
-                if (lane >= o) incl += y;
-            }
-            const unsigned hit = __ballot_sync(0xFFFFFFFFu, base + incl > u);
-            if (hit) {
-                const int src = __ffs(hit) - 1;
-                at = b0 + src;
-                base += __shfl_sync(0xFFFFFFFFu, incl - x, src);
-                break;
-            }
-            base += __shfl_sync(0xFFFFFFFFu, incl, 31);
+    {
+        long long x = x0, incl = incl0;
+        unsigned hit;
+        while (!(hit = __ballot_sync(0xFFFFFFFFu, before + incl > u))) {
+            before += __shfl_sync(0xFFFFFFFFu, incl, 31);
+            b += 32;
+            x = units(b, nullptr);
+            incl = upto(x);
         }
-        if (lane == 0) {
-            s_b = at;
-            s_mine = base;
-        }
+        const int src = __ffs(hit) - 1;
+        before += __shfl_sync(0xFFFFFFFFu, incl - x, src);
+        b += src;
     }
-    __syncthreads();
-    b = s_b;
-    before = s_mine;
 
     unsigned *tickets = static_cast<unsigned *>(a.ws);
     float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + a.ticket_bytes);
@@ -226,38 +232,38 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
         const int tok0 = (s.u0 + ua) * kUnit + warp * kTile;  // this warp's first tile; the next ones kUnit apart
         const int *table = p.table + (long long)b * p.max_pages;
         const int rpp = p.P / kBlk;
-        int pg = -1;  // lane i: page of record i (two a tile) of the 16 tiles from tile pg_at on
-        auto pages_from = [&](int it) {
-            const long long tok = tok0 + (long long)(it + (lane >> 1)) * kUnit + (lane & 1) * kBlk;
-            pg = -1;
-            if (it + (lane >> 1) < its && tok < s.len) {
-                pg = table[(int)(tok / p.P)];
-                if (pg < 0 || pg >= p.pages) {
-                    raise_flag(a.status, CG_FLAG_BATCH);
-                    pg = -1;
-                }
+        const uint8_t *heads = a.pool + (long long)kvh * rpp * RB;
+        long long at = -1;  // lane i: offset of record i (two a tile) of the 16 tiles last looked up, -1 where it has no page
+        auto look_up = [&](int it) {
+            const int rec = tok0 / kBlk + (it + (lane >> 1)) * (kUnit / kBlk) + (lane & 1);
+            at = -1;
+            if (it + (lane >> 1) < its && (long long)rec * kBlk < s.len) {
+                const int page = table[rec / rpp];
+                if (page < 0 || page >= p.pages) raise_flag(a.status, CG_FLAG_BATCH);
+                else at = page * p.page_stride + (long long)(rec % rpp) * RB;
             }
         };
         unsigned ok_now = 0;  // two bits a tile in the ring, by stage: records that have a page
         auto issue = [&](int it) {
-            if ((it & 15) == 0) pages_from(it);
+            if ((it & 15) == 0) look_up(it);
             const int st = it % ST;
-            const int p0 = __shfl_sync(0xFFFFFFFFu, pg, 2 * (it & 15)), p1 = __shfl_sync(0xFFFFFFFFu, pg, 2 * (it & 15) + 1);
-            ok_now = (ok_now & ~(3u << (2 * st))) | ((unsigned)((p0 >= 0) | ((p1 >= 0) << 1)) << (2 * st));
+            const long long a0 = __shfl_sync(0xFFFFFFFFu, at, 2 * (it & 15)), a1 = __shfl_sync(0xFFFFFFFFu, at, 2 * (it & 15) + 1);
+            ok_now = (ok_now & ~(3u << (2 * st))) | ((unsigned)((a0 >= 0) | ((a1 >= 0) << 1)) << (2 * st));
             if (it < its) {
-                const int r0 = (tok0 + it * kUnit) / kBlk;
-                const uint8_t *s0 = a.pool + p0 * p.page_stride + ((long long)kvh * rpp + r0 % rpp) * RB;
-                const uint8_t *s1 = a.pool + p1 * p.page_stride + ((long long)kvh * rpp + (r0 + 1) % rpp) * RB - RB;
-                const unsigned dst = ring_s + st * TB;
+                const uint8_t *s0 = heads + a0 + lane * 16, *s1 = heads + a1 - RB + lane * 16;
+                const unsigned dst = ring_s + st * TB + lane * 16;
 #pragma unroll
                 for (int c = 0; c < TB / 512; c++) {
-                    const int o = (c * 32 + lane) * 16;
-                    if (o < RB ? p0 >= 0 : p1 >= 0) copy16(dst + o, (o < RB ? s0 : s1) + o);
+                    if ((c + 1) * 512 <= RB) {  // wholly in the first record
+                        if (a0 >= 0) copy16(dst + c * 512, s0 + c * 512);
+                    } else if (c * 512 >= RB) {
+                        if (a1 >= 0) copy16(dst + c * 512, s1 + c * 512);
+                    } else {
+                        const bool one = c * 512 + lane * 16 < RB;
+                        if (one ? a0 >= 0 : a1 >= 0) copy16(dst + c * 512, (one ? s0 : s1) + c * 512);
+                    }
                 }
-                if (TB % 512 && lane < TB % 512 / 16) {
-                    const int o = (TB / 512 * 32 + lane) * 16;
-                    if (p1 >= 0) copy16(dst + o, s1 + o);
-                }
+                if (TB % 512 && lane < TB % 512 / 16 && a1 >= 0) copy16(dst + TB / 512 * 512, s1 + TB / 512 * 512);
             }
             copy_commit();
         };
@@ -298,7 +304,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
             // the column's largest goes to [2^13, 2^14)
             int kq = top > 0.0f ? 13 - ((int)(__float_as_uint(top) >> 23) - 127) : 0;
             kq = kq > 120 ? 120 : kq;
-            const float f = pow2f(kq);
+            const float f = a.scale < 0.0f ? -pow2f(kq) : pow2f(kq);
             float sums[NG];
 #pragma unroll
             for (int i = 0; i < NG; i++) sums[i] = 0.0f;
@@ -317,7 +323,8 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                 sums[i] += __shfl_xor_sync(0xFFFFFFFFu, sums[i], 1);
                 sums[i] += __shfl_xor_sync(0xFFFFFFFFu, sums[i], 2);
             }
-            const float back = a.scale * kLog2e * pow2f(24 - kq > 127 ? 127 : 24 - kq);
+            // never zero: a hidden score's -inf times it stays -inf
+            const float back = fmaxf(fabsf(a.scale) * kLog2e * pow2f(24 - kq > 127 ? 127 : 24 - kq), 1e-37f);
             // to the accumulators' columns 2t, 2t + 1
 #pragma unroll
             for (int c = 0; c < 2; c++) {
@@ -353,7 +360,10 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
             l[nt][0] = l[nt][1] = 0.0f;
             bits[nt][0] = bits[nt][1] = 0;
         }
-        int sig = kSigMin;  // every |V^| seen is below 2^(sig + 1)
+        int sig = kSigMin;       // every |V^| seen is below 2^(sig + 1) = limit
+        float limit = pow2f(kSigMin + 1), mtop[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) mtop[nt][0] = mtop[nt][1] = -INFINITY;  // m + 6
 
         for (int it = 0; it < its; it++) {
             copy_wait<ST - 2>();
@@ -418,67 +428,92 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                         }
                     }
                 }
-                // ---- base-2 scores, hidden ones -inf
+                // ---- hidden scores -inf
+                if (!plain) {
 #pragma unroll
-                for (int r = 0; r < 2; r++)
+                    for (int r = 0; r < 2; r++)
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++)
+                        for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                        for (int c = 0; c < 4; c++) {
-                            sc[r][nt][c] *= qscale[nt][c & 1];
-                            if (!plain) {
-                                const int at = tok + r * kBlk + (c >> 1) * 8 + g;
-                                if (!((okr >> r) & 1u) || at > hi[nt][c & 1] || at < lo[nt][c & 1])
-                                    sc[r][nt][c] = -INFINITY;
+                            for (int c = 0; c < 4; c++) {
+                                const int pos = tok + r * kBlk + (c >> 1) * 8 + g;
+                                if (!((okr >> r) & 1u) || pos > hi[nt][c & 1] || pos < lo[nt][c & 1]) sc[r][nt][c] = -INFINITY;
                             }
-                        }
+                }
                 // ---- value parameters of tokens 2t, 2t + 1, 8 + 2t, 8 + 2t + 1, this lane's group; sigma
                 float vs[2][4], vm[2][4];
-                float big = 0.0f;
-                bool odd = false;
+                float big = 0.0f, check = 0.0f;
 #pragma unroll
                 for (int r = 0; r < 2; r++) {
                     const unsigned *pv = reinterpret_cast<const unsigned *>(tile + r * RB + R::kPV) + g * (D / 8) / G;
 #pragma unroll
                     for (int i = 0; i < 4; i++) {
-                        const int tk = (i >> 1) * 8 + 2 * t + (i & 1);
-                        const unsigned w = pv[tk * NG];
-                        float sv = bits_to_float<BF>(w & 0xFFFFu), mv = bits_to_float<BF>(w >> 16);
-                        const bool fine = fabsf(sv) <= 3.402823466e38f && fabsf(mv) <= 3.402823466e38f;
-                        const bool held = ((okr >> r) & 1u) && tok + r * kBlk + tk < s.len;
-                        odd |= held && !fine;
-                        if (!fine || !held) sv = mv = 0.0f;
-                        vs[r][i] = sv;
-                        vm[r][i] = mv;
-                        big = fmaxf(big, fmaxf(fabsf(mv), fabsf(fmaf(15.0f, sv, mv))));
+                        const unsigned w = pv[((i >> 1) * 8 + 2 * t + (i & 1)) * NG];
+                        vs[r][i] = bits_to_float<BF>(w & 0xFFFFu);
+                        vm[r][i] = bits_to_float<BF>(w >> 16);
+                        check = fmaf(vs[r][i], 0.0f, check);  // NaN where a scale is not finite
+                        big = max3(big, fabsf(vm[r][i]), fabsf(fmaf(15.0f, vs[r][i], vm[r][i])));
                     }
                 }
-                const unsigned bu = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(big, 3.402823466e38f)));
-                const int e = max((int)(bu >> 23) - 127, kSigMin);
-                // ---- maxima; they follow the scores in steps of at least 6, so that accumulators are rarely rescaled
-                float mx[NT][2];
-                bool change = e > sig;
+                if (__any_sync(0xFFFFFFFFu, !plain || check != 0.0f)) {
+                    // slots that no sequence holds count as zero; so do groups that are not finite, whose channels are
+                    // remembered for the columns that see them
+                    big = 0.0f;
+                    bool odd = false;
+#pragma unroll
+                    for (int r = 0; r < 2; r++)
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            const bool held = ((okr >> r) & 1u) && tok + r * kBlk + (i >> 1) * 8 + 2 * t + (i & 1) < s.len;
+                            const bool fine = fabsf(vs[r][i]) <= 3.402823466e38f && fabsf(vm[r][i]) <= 3.402823466e38f;
+                            odd |= held && !fine;
+                            if (!fine || !held) vs[r][i] = vm[r][i] = 0.0f;
+                            big = fmaxf(big, fmaxf(fabsf(vm[r][i]), fabsf(fmaf(15.0f, vs[r][i], vm[r][i]))));
+                        }
+                    if (__any_sync(0xFFFFFFFFu, odd)) {
+#pragma unroll 1
+                        for (int r = 0; r < 2; r++)
+#pragma unroll 1
+                            for (int i = 0; i < NG; i++)
+#pragma unroll
+                                for (int k = 0; k < 2; k++) {
+                                    const unsigned w = reinterpret_cast<const unsigned *>(tile + r * RB + R::kPV)[(8 * k + g) * NG + i];
+                                    if (!(fabsf(bits_to_float<BF>(w & 0xFFFFu)) <= 3.402823466e38f))
+#pragma unroll
+                                        for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                                            for (int c = 0; c < 2; c++)
+                                                if ((r ? sc[1] : sc[0])[nt][2 * k + c] != -INFINITY) bits[nt][c] |= 1u << i;
+                                }
+                    }
+                }
+                // ---- maxima and sigma follow in steps of at least 6 (a factor of 2): as long as no lane's scores or values pass
+                // them by more, nothing is exchanged between lanes and no accumulator rescaled
+                bool change = big >= limit;
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++)
 #pragma unroll
-                    for (int c = 0; c < 2; c++) {
-                        float x = fmaxf(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]), fmaxf(sc[1][nt][c], sc[1][nt][2 + c]));
-                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
-                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
-                        x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
-                        mx[nt][c] = x > m[nt][c] + 6.0f ? x : m[nt][c];
-                        change |= mx[nt][c] != m[nt][c];
-                    }
+                    for (int c = 0; c < 2; c++)
+                        change |= max3(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]), sc[1][nt][c], sc[1][nt][2 + c]) * qscale[nt][c] > mtop[nt][c];
                 if (__any_sync(0xFFFFFFFFu, change)) {
-                    const int ns = max(e, sig);
+                    const unsigned bu = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(big, 3.402823466e38f)));
+                    const int ns = max(max((int)(bu >> 23) - 127, kSigMin), sig);
                     const float fs = sig - ns < -126 ? 0.0f : pow2f(sig - ns);
                     sig = ns;
+                    limit = ns < 127 ? pow2f(ns + 1) : INFINITY;
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                         for (int c = 0; c < 2; c++) {
-                            const float f = m[nt][c] == mx[nt][c] ? 1.0f : exp2_approx(m[nt][c] - mx[nt][c]);
-                            m[nt][c] = mx[nt][c];
+                            float x = max3(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]), sc[1][nt][c], sc[1][nt][2 + c]);
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 4));
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
+                            x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
+                            x = x == -INFINITY ? x : x * qscale[nt][c];
+                            const float nm = x > m[nt][c] + 6.0f ? x : m[nt][c];
+                            const float f = m[nt][c] == nm ? 1.0f : exp2_approx(m[nt][c] - nm);
+                            m[nt][c] = nm;
+                            mtop[nt][c] = nm + 6.0f;
                             l[nt][c] *= f;
 #pragma unroll
                             for (int j = 0; j < KS; j++) {
@@ -487,24 +522,9 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                             }
                         }
                 }
-                if (__any_sync(0xFFFFFFFFu, odd)) {  // groups that are not finite: remembered for the columns that see them
-#pragma unroll
-                    for (int r = 0; r < 2; r++)
-                        for (int i = 0; i < NG; i++)
-#pragma unroll
-                            for (int k = 0; k < 2; k++) {
-                                const unsigned w = reinterpret_cast<const unsigned *>(tile + r * RB + R::kPV)[(8 * k + g) * NG + i];
-                                if (!(fabsf(bits_to_float<BF>(w & 0xFFFFu)) <= 3.402823466e38f))
-#pragma unroll
-                                    for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                                        for (int c = 0; c < 2; c++)
-                                            if (sc[r][nt][2 * k + c] != -INFINITY) bits[nt][c] |= 1u << i;
-                            }
-                }
                 // ---- weights, values
                 // V^ 2^(-7 - sig), within (-2^-6, 2^-6): c 2^-24 times s 2^(17 - sig), below 2^16 since 15 s < 2^(sig + 2)
-                const float fs = pow2f(17 - sig);
+                const float fs = pow2f(17 - sig), fm = fs * 5.9604644775390625e-8f;
 #pragma unroll
                 for (int r = 0; r < 2; r++) {
                     unsigned pb[NT][2];
@@ -514,7 +534,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
 #pragma unroll
                         for (int c = 0; c < 4; c++) {
                             const float mm = m[nt][c & 1] == -INFINITY ? 0.0f : m[nt][c & 1];
-                            pr[c] = exp2_approx(sc[r][nt][c] - mm);
+                            pr[c] = exp2_approx(fmaf(sc[r][nt][c], qscale[nt][c & 1], -mm));
                             l[nt][c & 1] += pr[c];
                         }
                         pb[nt][0] = transposed(pack_half(pr[0], pr[1]));
@@ -525,9 +545,8 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                     for (int k = 0; k < 2; k++) {
                         const float x = vs[r][2 * k] * fs, y = vs[r][2 * k + 1] * fs;
                         s1[k] = pack_half(x, y);
-                        s16[k] = pack_half(x * 0.0625f, y * 0.0625f);
-                        mm2[k] = pack_half(vm[r][2 * k] * 5.9604644775390625e-8f * fs,
-                                           vm[r][2 * k + 1] * 5.9604644775390625e-8f * fs);
+                        s16[k] = mul_half(s1[k], 0x2C002C00u);  // 1/16
+                        mm2[k] = pack_half(vm[r][2 * k] * fm, vm[r][2 * k + 1] * fm);
                     }
                     const uint8_t *rec = tile + r * RB + R::kV;
                     constexpr int VW = D / 64;  // words of a token's piece
@@ -660,22 +679,33 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                     float top = -INFINITY, tl = 0.0f;
                     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
                     unsigned bb = 0;
-                    for (int k = 0; k < count; k++) {
-                        const float *src = partials + ((first_cta + k) * 2 + (k == 0 ? 1 : 0)) * PF;
-                        const float pm = __ldcg(src + COLS * D + 3 * c), pl = __ldcg(src + COLS * D + 3 * c + 1);
-                        const unsigned pbits = __float_as_uint(__ldcg(src + COLS * D + 3 * c + 2));
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + c * D + d));
-                        if (pm == -INFINITY && pl == 0.0f) continue;
-                        const float nt_ = fmaxf(top, pm);
-                        const float f0 = top == -INFINITY ? (tl == 0.0f ? 0.0f : 1.0f) : exp2_approx(top - nt_);
-                        const float f1 = pm == -INFINITY ? 1.0f : exp2_approx(pm - nt_);
-                        top = nt_;
-                        tl = tl * f0 + pl * f1;
-                        x.x = x.x * f0 + y.x * f1;
-                        x.y = x.y * f0 + y.y * f1;
-                        x.z = x.z * f0 + y.z * f1;
-                        x.w = x.w * f0 + y.w * f1;
-                        bb |= pbits;
+                    for (int k0 = 0; k0 < count; k0 += kJoin) {  // kJoin parts' loads in flight
+                        float pm[kJoin], pl[kJoin];
+                        unsigned pbits[kJoin];
+                        float4 y[kJoin];
+#pragma unroll
+                        for (int k = 0; k < kJoin; k++) {
+                            const int kk = min(k0 + k, count - 1);
+                            const float *src = partials + ((first_cta + kk) * 2 + (kk == 0 ? 1 : 0)) * PF;
+                            pm[k] = __ldcg(src + COLS * D + 3 * c);
+                            pl[k] = __ldcg(src + COLS * D + 3 * c + 1);
+                            pbits[k] = __float_as_uint(__ldcg(src + COLS * D + 3 * c + 2));
+                            y[k] = __ldcg(reinterpret_cast<const float4 *>(src + c * D + d));
+                        }
+#pragma unroll
+                        for (int k = 0; k < kJoin; k++) {
+                            if (k0 + k >= count || (pm[k] == -INFINITY && pl[k] == 0.0f)) continue;
+                            const float nt_ = fmaxf(top, pm[k]);
+                            const float f0 = top == -INFINITY ? (tl == 0.0f ? 0.0f : 1.0f) : exp2_approx(top - nt_);
+                            const float f1 = pm[k] == -INFINITY ? 1.0f : exp2_approx(pm[k] - nt_);
+                            top = nt_;
+                            tl = tl * f0 + pl[k] * f1;
+                            x.x = x.x * f0 + y[k].x * f1;
+                            x.y = x.y * f0 + y[k].y * f1;
+                            x.z = x.z * f0 + y[k].z * f1;
+                            x.w = x.w * f0 + y[k].w * f1;
+                            bb |= pbits[k];
+                        }
                     }
                     put_out<D, G, BF>(a, s, kvh, ct * COLS + c, d, x, top, tl, bb);
                 }

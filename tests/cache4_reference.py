@@ -112,7 +112,7 @@ def attention(q, k, v, pos, window, scale, params_k, out_step, codes_step=0.0):
     total = p.sum()
     out, lse = p @ v / total, top + np.log(total)
     u, h = 2.0 ** -24, 2.0 ** -11
-    ds = scale * ((D + 16) * 4 * u * (t @ np.abs(q)) + 2.0 ** -24 * np.abs(q).max() * t.sum(1)).max() + 8 * u * np.abs(s).max()
+    ds = abs(scale) * ((D + 16) * 4 * u * (t @ np.abs(q)) + 2.0 ** -24 * np.abs(q).max() * t.sum(1)).max() + 8 * u * np.abs(s).max()
     bound = (p @ np.abs(v) / total) * (2 * ds + 2 * h + 2.0 ** -19) + 2.0 ** -24 * len(k) * np.nanmax(np.abs(v)) / total
     bound = bound * (1 + out_step) + out_step * np.abs(out) + 2.0 ** -25
     return out, lse, bound, ds + 2.0 ** -20 + 2.0 ** -23 * abs(lse)

@@ -485,3 +485,14 @@ def test_wrapper_refusals(c4):
     with pytest.raises(ValueError):
         c4.Cache4(2, 4, 16, 2, 64, pool=cache.pool[:1])
     assert int(cache.status.item()) == 0
+
+
+@pytest.mark.parametrize("rows", [1, 5, 40])
+@pytest.mark.parametrize("scale", [0.0, -0.2])
+def test_scales_that_are_not_positive(c4, rows, scale):
+    """Equal weights (scale 0) and reversed ones."""
+    pr = Problem(c4, [(150, rows), (60, rows)], H=1, D=128, dtype=torch.float16, seed=4).fill()
+    q = cuda16(pr.rng.standard_normal((2 * rows, 4, 128)).astype(np.float32), pr.dtype)
+    out, lse = pr.cache.attend(q, pr.batch(), return_lse=True, scale=scale)
+    assert pr.flags() == 0
+    check_attention(pr, q, out, lse, scale=scale, sample=60)
