@@ -24,7 +24,9 @@ namespace {
 
 constexpr int kWarps = 4, kThreads = 32 * kWarps;
 constexpr int kTile = 32;              // tokens a warp takes at a time: two records
-constexpr int kJoin = 8;
+// What beginning an item costs a CTA (queries, first copies, joining its warps), in units: items are dealt out
+// as if they had that many more. Without it CTAs with many short items ended 1.35 times as late as the others.
+constexpr int kItemUnits = 3;
 constexpr int kUnit = kTile * kWarps;  // tokens the work is dealt out in
 constexpr int kSigMin = -110;            // values below 2^-115 or so lose bits
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
@@ -66,18 +68,46 @@ __device__ __forceinline__ unsigned mul_half(unsigned a, unsigned b) {
     asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
     return y;
 }
+__device__ __forceinline__ unsigned max_half(unsigned a, unsigned b) {  // NaNs kept
+    unsigned y;
+    asm("max.NaN.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
 __device__ __forceinline__ float exp2_approx(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
-__device__ __forceinline__ void copy16(unsigned smem, const uint8_t *g) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
+// One bulk copy; its bytes count on the mbarrier.
+__device__ __forceinline__ void copy_bulk(unsigned smem, const uint8_t *g, unsigned bytes, unsigned bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(smem), "l"(g),
+                 "r"(bytes), "r"(bar)
+                 : "memory");
 }
-__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copy_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+__device__ __forceinline__ void bar_init(unsigned bar) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], 1;" ::"r"(bar) : "memory");
+}
+__device__ __forceinline__ void bar_expect(unsigned bar, unsigned bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(bar), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ bool bar_try(unsigned bar, unsigned parity) {
+    unsigned ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+constexpr unsigned kWaitLimit = 1u << 20;  // polls; far above any real wait
+__device__ __forceinline__ void bar_wait(unsigned bar, unsigned parity, int32_t *status) {
+    for (unsigned i = 0; !bar_try(bar, parity); i++)
+        if (i >= kWaitLimit) {
+            raise_flag(status, CG_FLAG_TIMEOUT);
+            return;
+        }
 }
 __device__ __forceinline__ float pow2f(int e) {  // 2^e, e in [-126, 127]
     return __int_as_float((e + 127) << 23);
@@ -164,7 +194,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
     auto units = [&](int b0, int32_t *status) -> long long {
         if (b0 + lane >= p.B) return 0;
         const Seq s = seq_of(p, a, b0 + lane, COLS, status);
-        return (long long)s.units * s.tiles * p.H;
+        return (long long)(s.units + kItemUnits) * s.tiles * p.H;
     };
     auto upto = [&](long long x) {
 #pragma unroll
@@ -209,26 +239,67 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
 
     uint8_t *ring = smem + warp * ST * TB;
     const unsigned ring_s = (unsigned)__cvta_generic_to_shared(ring);
+    __shared__ __align__(8) uint64_t s_bars[kWarps][ST];
+    const unsigned bars = (unsigned)__cvta_generic_to_shared(s_bars[warp]);
+    if (lane == 0) {
+        for (int i = 0; i < ST; i++) bar_init(bars + 8 * i);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncwarp();
+    unsigned parity = 0;  // bit i: of the next wait on stage i
 
-    while (u < u_end) {
-        // ---- the item that unit u belongs to
+    // Items that this CTA shares with others: the one it finds begun, the one it leaves (first_cta < 0: none). Their
+    // tickets are drawn after all its work, with one fence.
+    struct Shared {
+        int first_cta, count, first, n, kvh, ct;
+    } shared[2];
+    shared[0].first_cta = shared[1].first_cta = -1;
+
+    for (; u < u_end;) {
+        // ---- the item that unit u belongs to; its first kItemUnits units are only its cost
         Seq s = seq_of(p, a, b, COLS, nullptr);
-        long long all = (long long)s.units * s.tiles * p.H;
+        long long all = (long long)(s.units + kItemUnits) * s.tiles * p.H;
         while (u - before >= all) {
             before += all;
             b++;
             s = seq_of(p, a, b, COLS, nullptr);
-            all = (long long)s.units * s.tiles * p.H;
+            all = (long long)(s.units + kItemUnits) * s.tiles * p.H;
         }
-        const int item = (int)((u - before) / s.units), ua = (int)((u - before) % s.units);
+        const int per = s.units + kItemUnits;
+        const int item = (int)quotient(u - before, per), from = (int)(u - before - (long long)item * per);
         const long long left = u_end - u;
-        const int ub = left < s.units - ua ? ua + (int)left : s.units;
+        const int to = left < per - from ? from + (int)left : per;
+        const int ua = max(from - kItemUnits, 0), ub = max(to - kItemUnits, 0), its = ub - ua;
+        const long long item_u0 = u - from + kItemUnits, item_u1 = u - from + per;  // its units that are work
+        u += to - from;
+        if (its == 0) continue;
         const int kvh = item % p.H, ct = item / p.H;
-        const long long item_u0 = u - ua, item_u1 = item_u0 + s.units;
         const long long pos0 = (long long)p.kv_len[b] - s.n;
+        if (lane == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring held accumulators
+
+        // ---- queries (the loads): column n = 8 nt + g of the fragment, channels 16j + 4t + 0..3 of step j
+        unsigned q[NT][KS][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            const int col = ct * COLS + nt * 8 + g, row = col / a.R, h = kvh * a.R + col % a.R;
+            const uint16_t *src = a.q + (long long)(s.first + row) * a.q_stride + (long long)h * D + 4 * t;
+#pragma unroll
+            for (int j = 0; j < KS; j++) {
+                q[nt][j][0] = q[nt][j][1] = 0;
+                if (row < s.n) {
+                    if (a.q_vec) {
+                        const uint2 w = *reinterpret_cast<const uint2 *>(src + 16 * j);
+                        q[nt][j][0] = w.x;
+                        q[nt][j][1] = w.y;
+                    } else {
+                        q[nt][j][0] = src[16 * j] | ((unsigned)src[16 * j + 1] << 16);
+                        q[nt][j][1] = src[16 * j + 2] | ((unsigned)src[16 * j + 3] << 16);
+                    }
+                }
+            }
+        }
 
         // ---- copies of the first tiles
-        const int its = ub - ua;
         const int tok0 = (s.u0 + ua) * kUnit + warp * kTile;  // this warp's first tile; the next ones kUnit apart
         const int *table = p.table + (long long)b * p.max_pages;
         const int rpp = p.P / kBlk;
@@ -244,61 +315,35 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
             }
         };
         unsigned ok_now = 0;  // two bits a tile in the ring, by stage: records that have a page
+        int st_in = 0, st = 0;  // stages of the next tile to copy, to use
         auto issue = [&](int it) {
+            if (it >= its) return;
             if ((it & 15) == 0) look_up(it);
-            const int st = it % ST;
             const long long a0 = __shfl_sync(0xFFFFFFFFu, at, 2 * (it & 15)), a1 = __shfl_sync(0xFFFFFFFFu, at, 2 * (it & 15) + 1);
-            ok_now = (ok_now & ~(3u << (2 * st))) | ((unsigned)((a0 >= 0) | ((a1 >= 0) << 1)) << (2 * st));
-            if (it < its) {
-                const uint8_t *s0 = heads + a0 + lane * 16, *s1 = heads + a1 - RB + lane * 16;
-                const unsigned dst = ring_s + st * TB + lane * 16;
-#pragma unroll
-                for (int c = 0; c < TB / 512; c++) {
-                    if ((c + 1) * 512 <= RB) {  // wholly in the first record
-                        if (a0 >= 0) copy16(dst + c * 512, s0 + c * 512);
-                    } else if (c * 512 >= RB) {
-                        if (a1 >= 0) copy16(dst + c * 512, s1 + c * 512);
-                    } else {
-                        const bool one = c * 512 + lane * 16 < RB;
-                        if (one ? a0 >= 0 : a1 >= 0) copy16(dst + c * 512, (one ? s0 : s1) + c * 512);
-                    }
-                }
-                if (TB % 512 && lane < TB % 512 / 16 && a1 >= 0) copy16(dst + TB / 512 * 512, s1 + TB / 512 * 512);
+            const unsigned ok = (unsigned)((a0 >= 0) | ((a1 >= 0) << 1));
+            ok_now = (ok_now & ~(3u << (2 * st_in))) | (ok << (2 * st_in));
+            if (lane == 0) {
+                const unsigned bar = bars + 8 * st_in, dst = ring_s + st_in * TB;
+                bar_expect(bar, ok == 3u ? 2 * RB : ok ? RB : 0);
+                if (a0 >= 0) copy_bulk(dst, heads + a0, RB, bar);
+                if (a1 >= 0) copy_bulk(dst + RB, heads + a1, RB, bar);
             }
-            copy_commit();
+            st_in = st_in + 1 == ST ? 0 : st_in + 1;
         };
 #pragma unroll
         for (int i = 0; i < ST - 1; i++) issue(i);
 
-        // ---- queries: column n = 8 nt + g of the fragment, channels 16j + 4t + 0..3 of step j, under 2^kq of the column's own
-        unsigned q[NT][KS][2];
+        // ---- queries: under 2^kq of the column's own
         float qsum[NT][NG][2], qscale[NT][2];
         int hi[NT][2], lo[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
-            const int col = ct * COLS + nt * 8 + g, row = col / a.R, h = kvh * a.R + col % a.R;
-            const bool have = row < s.n;
-            const uint16_t *src = a.q + (long long)(s.first + row) * a.q_stride + (long long)h * D + 4 * t;
             float top = 0.0f;
-            unsigned raw[KS][2];
 #pragma unroll
-            for (int j = 0; j < KS; j++) {
-                raw[j][0] = raw[j][1] = 0;
-                if (have) {
-                    if (a.q_vec) {
-                        const uint2 w = *reinterpret_cast<const uint2 *>(src + 16 * j);
-                        raw[j][0] = w.x;
-                        raw[j][1] = w.y;
-                    } else {
-                        raw[j][0] = src[16 * j] | ((unsigned)src[16 * j + 1] << 16);
-                        raw[j][1] = src[16 * j + 2] | ((unsigned)src[16 * j + 3] << 16);
-                    }
-                }
+            for (int j = 0; j < KS; j++)
 #pragma unroll
                 for (int i = 0; i < 2; i++)
-                    top = fmaxf(top, fmaxf(fabsf(bits_to_float<BF>(raw[j][i] & 0xFFFFu)),
-                                           fabsf(bits_to_float<BF>(raw[j][i] >> 16))));
-            }
+                    top = max3(top, fabsf(bits_to_float<BF>(q[nt][j][i] & 0xFFFFu)), fabsf(bits_to_float<BF>(q[nt][j][i] >> 16)));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
             // the column's largest goes to [2^13, 2^14)
@@ -310,8 +355,8 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
             for (int i = 0; i < NG; i++) sums[i] = 0.0f;
 #pragma unroll
             for (int j = 0; j < KS; j++) {
-                float x[4] = {bits_to_float<BF>(raw[j][0] & 0xFFFFu), bits_to_float<BF>(raw[j][0] >> 16),
-                              bits_to_float<BF>(raw[j][1] & 0xFFFFu), bits_to_float<BF>(raw[j][1] >> 16)};
+                const float x[4] = {bits_to_float<BF>(q[nt][j][0] & 0xFFFFu), bits_to_float<BF>(q[nt][j][0] >> 16),
+                                    bits_to_float<BF>(q[nt][j][1] & 0xFFFFu), bits_to_float<BF>(q[nt][j][1] >> 16)};
                 q[nt][j][0] = pack_half(x[0] * f, x[1] * f);
                 q[nt][j][1] = pack_half(x[2] * f * 0.0625f, x[3] * f * 0.0625f);  // meets codes 16 times too large
                 const float2 y = __half22float2(*reinterpret_cast<__half2 *>(&q[nt][j][0]));
@@ -360,19 +405,20 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
             l[nt][0] = l[nt][1] = 0.0f;
             bits[nt][0] = bits[nt][1] = 0;
         }
-        int sig = kSigMin;       // every |V^| seen is below 2^(sig + 1) = limit
-        float limit = pow2f(kSigMin + 1), mtop[NT][2];
+        int sig = kSigMin;  // every |m| seen is below 2^sig, every s below 2^(sig - 2): |V^| < 5 2^sig
+        float mtop[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) mtop[nt][0] = mtop[nt][1] = -INFINITY;  // m + 6
 
         for (int it = 0; it < its; it++) {
-            copy_wait<ST - 2>();
-            __syncwarp();
-            const int st = it % ST;
+            bar_wait(bars + 8 * st, (parity >> st) & 1u, a.status);
+            parity ^= 1u << st;
+            __syncwarp();  // every lane has left the tile before
             const uint8_t *tile = ring + st * TB;
             const int tok = tok0 + it * kUnit;
             const unsigned okr = (ok_now >> (2 * st)) & 3u;
-            issue(it + ST - 1);  // into the stage of the tile before, which every lane has left
+            issue(it + ST - 1);  // into that one's stage
+            st = st + 1 == ST ? 0 : st + 1;
             const bool plain = okr == 3u && tok >= lo_max && tok + kTile - 1 <= hi_min;
             if (okr != 0u && tok < s.len) {
                 float sc[2][NT][4];
@@ -396,7 +442,24 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                             kb[i] = y.x, kb[i + 1] = y.y, kb[i + 2] = y.z, kb[i + 3] = y.w;
                         }
                     }
-                    const unsigned *pk = reinterpret_cast<const unsigned *>(rec + R::kPK);
+                    unsigned ppa[NG], ppb[NG];  // parameters of tokens g, 8 + g
+                    {
+                        const uint8_t *pk = rec + R::kPK + g * NG * 4;
+                        if (NG == 1) {
+                            ppa[0] = *reinterpret_cast<const unsigned *>(pk);
+                            ppb[0] = *reinterpret_cast<const unsigned *>(pk + 32);
+                        } else if (NG == 2) {
+                            const uint2 x = *reinterpret_cast<const uint2 *>(pk), y = *reinterpret_cast<const uint2 *>(pk + 64);
+                            ppa[0] = x.x, ppa[1 % NG] = x.y, ppb[0] = y.x, ppb[1 % NG] = y.y;
+                        } else {
+#pragma unroll
+                            for (int i = 0; i < NG; i += 4) {
+                                const uint4 x = *reinterpret_cast<const uint4 *>(pk + 4 * i), y = *reinterpret_cast<const uint4 *>(pk + 32 * NG + 4 * i);
+                                ppa[i] = x.x, ppa[(i + 1) % NG] = x.y, ppa[(i + 2) % NG] = x.z, ppa[(i + 3) % NG] = x.w;
+                                ppb[i] = y.x, ppb[(i + 1) % NG] = y.y, ppb[(i + 2) % NG] = y.z, ppb[(i + 3) % NG] = y.w;
+                            }
+                        }
+                    }
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) sc[r][nt][0] = sc[r][nt][1] = sc[r][nt][2] = sc[r][nt][3] = 0.0f;
 #pragma unroll
@@ -415,7 +478,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                                     q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
                             }
                         }
-                        const unsigned pa = pk[g * NG + i], pb = pk[(8 + g) * NG + i];
+                        const unsigned pa = ppa[i], pb = ppb[i];
                         const float s0 = bits_to_float<BF>(pa & 0xFFFFu), m0 = bits_to_float<BF>(pa >> 16);
                         const float s1 = bits_to_float<BF>(pb & 0xFFFFu), m1 = bits_to_float<BF>(pb >> 16);
 #pragma unroll
@@ -440,41 +503,61 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                                 if (!((okr >> r) & 1u) || pos > hi[nt][c & 1] || pos < lo[nt][c & 1]) sc[r][nt][c] = -INFINITY;
                             }
                 }
-                // ---- value parameters of tokens 2t, 2t + 1, 8 + 2t, 8 + 2t + 1, this lane's group; sigma
-                float vs[2][4], vm[2][4];
-                float big = 0.0f, check = 0.0f;
+                // ---- value parameters of tokens 2t, 2t + 1 (k = 0) and 8 + 2t, 8 + 2t + 1 (k = 1), this lane's group, as operands:
+                // V^ 2^(-7 - sig), within (-2^-6, 2^-6), is c 2^-24 times s 2^(17 - sig) and m 2^(-7 - sig)
+                unsigned s1[2][2], mm2[2][2];
+                auto params = [&](int r, int i, float &s, float &m) {
+                    const unsigned w = reinterpret_cast<const unsigned *>(tile + r * RB + R::kPV)[((i >> 1) * 8 + 2 * t + (i & 1)) * NG + g * (D / 8) / G];
+                    s = bits_to_float<BF>(w & 0xFFFFu);
+                    m = bits_to_float<BF>(w >> 16);
+                };
+                unsigned ms = 0, mm = 0;  // the largest of each, NaNs kept
+                {
+                    const float fs = pow2f(17 - sig), fm = fs * 5.9604644775390625e-8f;
 #pragma unroll
-                for (int r = 0; r < 2; r++) {
-                    const unsigned *pv = reinterpret_cast<const unsigned *>(tile + r * RB + R::kPV) + g * (D / 8) / G;
+                    for (int r = 0; r < 2; r++)
 #pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const unsigned w = pv[((i >> 1) * 8 + 2 * t + (i & 1)) * NG];
-                        vs[r][i] = bits_to_float<BF>(w & 0xFFFFu);
-                        vm[r][i] = bits_to_float<BF>(w >> 16);
-                        check = fmaf(vs[r][i], 0.0f, check);  // NaN where a scale is not finite
-                        big = max3(big, fabsf(vm[r][i]), fabsf(fmaf(15.0f, vs[r][i], vm[r][i])));
-                    }
+                        for (int k = 0; k < 2; k++) {
+                            float sa, ma, sb, mb;
+                            params(r, 2 * k, sa, ma);
+                            params(r, 2 * k + 1, sb, mb);
+                            s1[r][k] = pack_half(sa * fs, sb * fs);
+                            mm2[r][k] = pack_half(ma * fm, mb * fm);
+                            ms = max_half(ms, s1[r][k]);
+                            mm = max_half(mm, mm2[r][k] & 0x7FFF7FFFu);
+                        }
                 }
-                if (__any_sync(0xFFFFFFFFu, !plain || check != 0.0f)) {
+                // maxima follow in steps of at least 6, sigma in factors of two: as long as no lane's scores or values pass
+                // them by more, nothing is exchanged between lanes and no accumulator is rescaled. Values stay below their
+                // limit while m 2^(-7 - sig) < 2^-7 and 15 s 2^(17 - sig) < 2^17; the test of bit patterns also finds NaNs.
+                const unsigned over = ((ms + 0x08000800u) | (mm + 0x60006000u)) & 0x80008000u;
+                bool change = over != 0;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int c = 0; c < 2; c++)
+                        change |= max3(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]), sc[1][nt][c], sc[1][nt][2 + c]) * qscale[nt][c] > mtop[nt][c];
+                if (__any_sync(0xFFFFFFFFu, change || !plain)) {
                     // slots that no sequence holds count as zero; so do groups that are not finite, whose channels are
                     // remembered for the columns that see them
-                    big = 0.0f;
+                    float vs[2][4], vm[2][4], big = 0.0f;
                     bool odd = false;
 #pragma unroll
                     for (int r = 0; r < 2; r++)
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
+                            params(r, i, vs[r][i], vm[r][i]);
                             const bool held = ((okr >> r) & 1u) && tok + r * kBlk + (i >> 1) * 8 + 2 * t + (i & 1) < s.len;
                             const bool fine = fabsf(vs[r][i]) <= 3.402823466e38f && fabsf(vm[r][i]) <= 3.402823466e38f;
                             odd |= held && !fine;
                             if (!fine || !held) vs[r][i] = vm[r][i] = 0.0f;
-                            big = fmaxf(big, fmaxf(fabsf(vm[r][i]), fabsf(fmaf(15.0f, vs[r][i], vm[r][i]))));
+                            big = max3(big, 2.0f * fabsf(vm[r][i]), 8.0f * vs[r][i]);
                         }
                     if (__any_sync(0xFFFFFFFFu, odd)) {
 #pragma unroll 1
-                        for (int r = 0; r < 2; r++)
-#pragma unroll 1
-                            for (int i = 0; i < NG; i++)
+                        for (int i = 0; i < NG; i++)
+#pragma unroll
+                            for (int r = 0; r < 2; r++)
 #pragma unroll
                                 for (int k = 0; k < 2; k++) {
                                     const unsigned w = reinterpret_cast<const unsigned *>(tile + r * RB + R::kPV)[(8 * k + g) * NG + i];
@@ -483,24 +566,21 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                                         for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                                             for (int c = 0; c < 2; c++)
-                                                if ((r ? sc[1] : sc[0])[nt][2 * k + c] != -INFINITY) bits[nt][c] |= 1u << i;
+                                                if (sc[r][nt][2 * k + c] != -INFINITY) bits[nt][c] |= 1u << i;
                                 }
                     }
-                }
-                // ---- maxima and sigma follow in steps of at least 6 (a factor of 2): as long as no lane's scores or values pass
-                // them by more, nothing is exchanged between lanes and no accumulator rescaled
-                bool change = big >= limit;
-#pragma unroll
-                for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                    for (int c = 0; c < 2; c++)
-                        change |= max3(fmaxf(sc[0][nt][c], sc[0][nt][2 + c]), sc[1][nt][c], sc[1][nt][2 + c]) * qscale[nt][c] > mtop[nt][c];
-                if (__any_sync(0xFFFFFFFFu, change)) {
                     const unsigned bu = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(big, 3.402823466e38f)));
-                    const int ns = max(max((int)(bu >> 23) - 127, kSigMin), sig);
-                    const float fs = sig - ns < -126 ? 0.0f : pow2f(sig - ns);
+                    const int ns = max(max((int)(bu >> 23) - 127, kSigMin), sig);  // |m| < 2^ns, s < 2^(ns - 2)
+                    const float fo = sig - ns < -126 ? 0.0f : pow2f(sig - ns);
                     sig = ns;
-                    limit = ns < 127 ? pow2f(ns + 1) : INFINITY;
+                    const float fs = pow2f(17 - sig), fm = fs * 5.9604644775390625e-8f;
+#pragma unroll
+                    for (int r = 0; r < 2; r++)
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            s1[r][k] = pack_half(vs[r][2 * k] * fs, vs[r][2 * k + 1] * fs);
+                            mm2[r][k] = pack_half(vm[r][2 * k] * fm, vm[r][2 * k + 1] * fm);
+                        }
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++)
 #pragma unroll
@@ -517,14 +597,12 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                             l[nt][c] *= f;
 #pragma unroll
                             for (int j = 0; j < KS; j++) {
-                                o[nt][j][c] *= f * fs;
-                                o[nt][j][2 + c] *= f * fs;
+                                o[nt][j][c] *= f * fo;
+                                o[nt][j][2 + c] *= f * fo;
                             }
                         }
                 }
                 // ---- weights, values
-                // V^ 2^(-7 - sig), within (-2^-6, 2^-6): c 2^-24 times s 2^(17 - sig), below 2^16 since 15 s < 2^(sig + 2)
-                const float fs = pow2f(17 - sig), fm = fs * 5.9604644775390625e-8f;
 #pragma unroll
                 for (int r = 0; r < 2; r++) {
                     unsigned pb[NT][2];
@@ -540,14 +618,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                         pb[nt][0] = transposed(pack_half(pr[0], pr[1]));
                         pb[nt][1] = transposed(pack_half(pr[2], pr[3]));
                     }
-                    unsigned s1[2], s16[2], mm2[2];
-#pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        const float x = vs[r][2 * k] * fs, y = vs[r][2 * k + 1] * fs;
-                        s1[k] = pack_half(x, y);
-                        s16[k] = mul_half(s1[k], 0x2C002C00u);  // 1/16
-                        mm2[k] = pack_half(vm[r][2 * k] * fm, vm[r][2 * k + 1] * fm);
-                    }
+                    const unsigned s16[2] = {mul_half(s1[r][0], 0x2C002C00u), mul_half(s1[r][1], 0x2C002C00u)};  // / 16
                     const uint8_t *rec = tile + r * RB + R::kV;
                     constexpr int VW = D / 64;  // words of a token's piece
                     unsigned va[2][2 * VW > 4 ? 2 * VW : 4];
@@ -573,10 +644,10 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                             unsigned x1 = __byte_perm(va[1][w], va[1][VW + w], y ? 0x7632 : 0x5410);
 #pragma unroll
                             for (int z = 0; z < 2; z++) {
-                                const unsigned a0 = fma_half(x0 & 0x000F000Fu, s1[0], mm2[0]);
-                                const unsigned a1 = fma_half(x0 & 0x00F000F0u, s16[0], mm2[0]);
-                                const unsigned a2 = fma_half(x1 & 0x000F000Fu, s1[1], mm2[1]);
-                                const unsigned a3 = fma_half(x1 & 0x00F000F0u, s16[1], mm2[1]);
+                                const unsigned a0 = fma_half(x0 & 0x000F000Fu, s1[r][0], mm2[r][0]);
+                                const unsigned a1 = fma_half(x0 & 0x00F000F0u, s16[0], mm2[r][0]);
+                                const unsigned a2 = fma_half(x1 & 0x000F000Fu, s1[r][1], mm2[r][1]);
+                                const unsigned a3 = fma_half(x1 & 0x00F000F0u, s16[1], mm2[r][1]);
 #pragma unroll
                                 for (int nt = 0; nt < NT; nt++)
                                     mma(o[nt][(w * 2 + y) * 2 + z], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
@@ -587,7 +658,6 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                 }
             }
         }
-        copy_wait<0>();
 
         // ---- join the warps: accumulators through shared memory in the ring's place
 #pragma unroll
@@ -660,59 +730,93 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
             }
         }
         if (!whole) {
-            // the CTAs that share the item are those whose ranges meet it
-            const long long first_cta = cta_of(item_u0, total, grid), last_cta = cta_of(item_u1 - 1, total, grid);
-            const int count = (int)(last_cta - first_cta + 1);
-            __threadfence();
-            __syncthreads();
-            if (threadIdx.x == 0) {
-                // tickets: one a CTA; the item's is that of the first CTA that has a part of it, which ends there
-                const unsigned was = atomicAdd(tickets + first_cta, 1u);
-                s_last = was == (unsigned)(count - 1);
-                if (s_last) tickets[first_cta] = 0;
-            }
-            __syncthreads();
-            if (s_last) {
-                __threadfence();
-                for (int i = threadIdx.x; i < ncols * Q4; i += kThreads) {
-                    const int c = i / Q4, d = (i % Q4) * 4;
-                    float top = -INFINITY, tl = 0.0f;
-                    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-                    unsigned bb = 0;
-                    for (int k0 = 0; k0 < count; k0 += kJoin) {  // kJoin parts' loads in flight
-                        float pm[kJoin], pl[kJoin];
-                        unsigned pbits[kJoin];
-                        float4 y[kJoin];
-#pragma unroll
-                        for (int k = 0; k < kJoin; k++) {
-                            const int kk = min(k0 + k, count - 1);
-                            const float *src = partials + ((first_cta + kk) * 2 + (kk == 0 ? 1 : 0)) * PF;
-                            pm[k] = __ldcg(src + COLS * D + 3 * c);
-                            pl[k] = __ldcg(src + COLS * D + 3 * c + 1);
-                            pbits[k] = __float_as_uint(__ldcg(src + COLS * D + 3 * c + 2));
-                            y[k] = __ldcg(reinterpret_cast<const float4 *>(src + c * D + d));
-                        }
-#pragma unroll
-                        for (int k = 0; k < kJoin; k++) {
-                            if (k0 + k >= count || (pm[k] == -INFINITY && pl[k] == 0.0f)) continue;
-                            const float nt_ = fmaxf(top, pm[k]);
-                            const float f0 = top == -INFINITY ? (tl == 0.0f ? 0.0f : 1.0f) : exp2_approx(top - nt_);
-                            const float f1 = pm[k] == -INFINITY ? 1.0f : exp2_approx(pm[k] - nt_);
-                            top = nt_;
-                            tl = tl * f0 + pl[k] * f1;
-                            x.x = x.x * f0 + y[k].x * f1;
-                            x.y = x.y * f0 + y[k].y * f1;
-                            x.z = x.z * f0 + y[k].z * f1;
-                            x.w = x.w * f0 + y[k].w * f1;
-                            bb |= pbits[k];
-                        }
-                    }
-                    put_out<D, G, BF>(a, s, kvh, ct * COLS + c, d, x, top, tl, bb);
-                }
-            }
+            const int first_cta = (int)cta_of(item_u0, total, grid);
+            shared[ua == 0] = {first_cta, (int)cta_of(item_u1 - 1, total, grid) - first_cta + 1, s.first, s.n, kvh, ct};
         }
         __syncthreads();  // the ring is free again
-        u += its;
+    }
+
+    // ---- shared items: the last CTA to draw an item's ticket joins its parts, in the order of the ranges. The ticket
+    // is that of the item's first CTA, which it is the last item of.
+    if (shared[0].first_cta < 0 && shared[1].first_cta < 0) return;
+    if (threadIdx.x == 0) {  // after the barrier: what the whole CTA wrote
+        __threadfence();
+        int last = 0;
+#pragma unroll
+        for (int i = 0; i < 2; i++)
+            if (shared[i].first_cta >= 0) {
+                const unsigned was = atomicAdd(tickets + shared[i].first_cta, 1u);
+                if (was == (unsigned)(shared[i].count - 1)) {
+                    last |= 1 << i;
+                    tickets[shared[i].first_cta] = 0;
+                }
+            }
+        __threadfence();
+        s_last = last;
+    }
+    __syncthreads();
+#pragma unroll 1
+    for (int i = 0; i < 2; i++) {
+        if (!((s_last >> i) & 1)) continue;
+        const Shared h = i ? shared[1] : shared[0];
+        const int ncols = min(COLS, h.n * a.R - h.ct * COLS);
+        constexpr int L4 = D / 4 < 32 ? D / 4 : 32, PER = D / 4 / L4;  // lanes of a column, groups of 4 channels a lane
+        // a warp a column: lane k has part k's maximum and sum, then all lanes add up the parts' channels
+        for (int c = warp; c < ncols; c += kWarps) {
+            auto part_of = [&](int k) { return partials + ((long long)(h.first_cta + k) * 2 + (k == 0 ? 1 : 0)) * PF; };
+            float top = -INFINITY, tl = 0.0f;
+            float4 x[PER];
+            unsigned bb = 0;
+#pragma unroll
+            for (int j = 0; j < PER; j++) x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int k0 = 0; k0 < h.count; k0 += 32) {
+                float pm = -INFINITY, pl = 0.0f;
+                if (k0 + lane < h.count) {
+                    const float *tail = part_of(k0 + lane) + COLS * D + 3 * c;
+                    pm = __ldcg(tail);
+                    pl = __ldcg(tail + 1);
+                    bb |= __float_as_uint(__ldcg(tail + 2));
+                }
+                float nm = fmaxf(top, pm);
+#pragma unroll
+                for (int o = 16; o; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xFFFFFFFFu, nm, o));
+                const float base = nm == -INFINITY ? 0.0f : nm;
+                const float f0 = top == -INFINITY && tl == 0.0f ? 0.0f : exp2_approx((top == -INFINITY ? base : top) - base);
+                float f = pm == -INFINITY && pl == 0.0f ? 0.0f : exp2_approx((pm == -INFINITY ? base : pm) - base);
+                float sum = pl * f;
+#pragma unroll
+                for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+                tl = tl * f0 + sum;
+                top = nm;
+#pragma unroll
+                for (int j = 0; j < PER; j++) x[j].x *= f0, x[j].y *= f0, x[j].z *= f0, x[j].w *= f0;
+                const int many = min(32, h.count - k0);
+#pragma unroll 1
+                for (int k = 0; k < many; k += 8) {
+                    float4 y[8][PER];
+#pragma unroll
+                    for (int e = 0; e < 8; e++)
+#pragma unroll
+                        for (int j = 0; j < PER; j++)
+                            y[e][j] = __ldcg(reinterpret_cast<const float4 *>(part_of(k0 + min(k + e, many - 1)) + c * D) + j * L4 + lane % L4);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        const float fe = __shfl_sync(0xFFFFFFFFu, f, (k + e) & 31);
+                        if (k + e < many && fe != 0.0f) {
+#pragma unroll
+                            for (int j = 0; j < PER; j++)
+                                x[j].x += y[e][j].x * fe, x[j].y += y[e][j].y * fe, x[j].z += y[e][j].z * fe, x[j].w += y[e][j].w * fe;
+                        }
+                    }
+                }
+            }
+            bb = __reduce_or_sync(0xFFFFFFFFu, bb);
+            Seq s;
+            s.first = h.first;
+            if (lane < L4)
+#pragma unroll
+                for (int j = 0; j < PER; j++) put_out<D, G, BF>(a, s, h.kvh, h.ct * COLS + c, (j * L4 + lane) * 4, x[j], top, tl, bb);
+        }
     }
 }
 
