@@ -113,6 +113,23 @@ __device__ __forceinline__ float pow2f(int e) {  // 2^e, e in [-126, 127]
     return __int_as_float((e + 127) << 23);
 }
 
+// W consecutive words of shared memory.
+template <int W>
+__device__ __forceinline__ void load_words(const uint8_t *p, unsigned *x) {
+    if (W == 1) {
+        x[0] = *reinterpret_cast<const unsigned *>(p);
+    } else if (W == 2) {
+        const uint2 y = *reinterpret_cast<const uint2 *>(p);
+        x[0] = y.x, x[1 % W] = y.y;
+    } else {
+#pragma unroll
+        for (int i = 0; i < W; i += 4) {
+            const uint4 y = *reinterpret_cast<const uint4 *>(p + 4 * i);
+            x[i] = y.x, x[(i + 1) % W] = y.y, x[(i + 2) % W] = y.z, x[(i + 3) % W] = y.w;
+        }
+    }
+}
+
 // What a sequence asks of the call.
 struct Seq {
     int first, n;      // rows
@@ -422,74 +439,54 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
             const bool plain = okr == 3u && tok >= lo_max && tok + kTile - 1 <= hi_min;
             if (okr != 0u && tok < s.len) {
                 float sc[2][NT][4];
+                unsigned kc[2][2][W], kp[2][2][NG];  // codes and parameters of tokens g, 8 + g of either record
 #pragma unroll
-                for (int r = 0; r < 2; r++) {
-                    const uint8_t *rec = tile + r * RB;
-                    unsigned ka[W], kb[W];
+                for (int r = 0; r < 2; r++)
 #pragma unroll
-                    for (int i = 0; i < W; i++) {
-                        // vector loads of the lane's chunk: tokens g and 8 + g
-                        if (W == 2) {
-                            if (i == 0) {
-                                const uint2 x = *reinterpret_cast<const uint2 *>(rec + lane * (D / 8));
-                                const uint2 y = *reinterpret_cast<const uint2 *>(rec + 4 * D + lane * (D / 8));
-                                ka[0] = x.x, ka[1] = x.y, kb[0] = y.x, kb[1] = y.y;
-                            }
-                        } else if (i % 4 == 0) {
-                            const uint4 x = *reinterpret_cast<const uint4 *>(rec + lane * (D / 8) + 4 * i);
-                            const uint4 y = *reinterpret_cast<const uint4 *>(rec + 4 * D + lane * (D / 8) + 4 * i);
-                            ka[i] = x.x, ka[i + 1] = x.y, ka[i + 2] = x.z, ka[i + 3] = x.w;
-                            kb[i] = y.x, kb[i + 1] = y.y, kb[i + 2] = y.z, kb[i + 3] = y.w;
-                        }
+                    for (int h = 0; h < 2; h++) {
+                        load_words<W>(tile + r * RB + h * 4 * D + lane * (D / 8), kc[r][h]);
+                        load_words<NG>(tile + r * RB + R::kPK + (8 * h + g) * NG * 4, kp[r][h]);
                     }
-                    unsigned ppa[NG], ppb[NG];  // parameters of tokens g, 8 + g
-                    {
-                        const uint8_t *pk = rec + R::kPK + g * NG * 4;
-                        if (NG == 1) {
-                            ppa[0] = *reinterpret_cast<const unsigned *>(pk);
-                            ppb[0] = *reinterpret_cast<const unsigned *>(pk + 32);
-                        } else if (NG == 2) {
-                            const uint2 x = *reinterpret_cast<const uint2 *>(pk), y = *reinterpret_cast<const uint2 *>(pk + 64);
-                            ppa[0] = x.x, ppa[1 % NG] = x.y, ppb[0] = y.x, ppb[1 % NG] = y.y;
-                        } else {
+                // Groups two at a time: with both records four chains of matrix instructions, in turn, since each waits
+                // for the one before it in its own chain.
+                constexpr int GB = NG < 2 ? NG : 2;
 #pragma unroll
-                            for (int i = 0; i < NG; i += 4) {
-                                const uint4 x = *reinterpret_cast<const uint4 *>(pk + 4 * i), y = *reinterpret_cast<const uint4 *>(pk + 32 * NG + 4 * i);
-                                ppa[i] = x.x, ppa[(i + 1) % NG] = x.y, ppa[(i + 2) % NG] = x.z, ppa[(i + 3) % NG] = x.w;
-                                ppb[i] = y.x, ppb[(i + 1) % NG] = y.y, ppb[(i + 2) % NG] = y.z, ppb[(i + 3) % NG] = y.w;
-                            }
+                for (int i0 = 0; i0 < NG; i0 += GB) {
+                    float dot[2][GB][NT][4];
+#pragma unroll
+                    for (int w = 0; w < G / 32; w++)
+#pragma unroll
+                        for (int half = 0; half < 2; half++)
+#pragma unroll
+                            for (int r = 0; r < 2; r++)
+#pragma unroll
+                                for (int i = 0; i < GB; i++) {
+                                    const int at = (i0 + i) * G / 32 + w;
+                                    const unsigned x = kc[r][0][at] >> (8 * half), y = kc[r][1][at] >> (8 * half);
+#pragma unroll
+                                    for (int nt = 0; nt < NT; nt++) {
+                                        float *d = dot[r][i][nt];
+                                        if (w + half == 0) d[0] = d[1] = d[2] = d[3] = 0.0f;
+                                        mma(d, x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u,
+                                            q[nt][2 * at + half][0], q[nt][2 * at + half][1]);
+                                    }
+                                }
+#pragma unroll
+                    for (int r = 0; r < 2; r++)
+#pragma unroll
+                        for (int i = 0; i < GB; i++) {
+                            const unsigned pa = kp[r][0][i0 + i], pb = kp[r][1][i0 + i];
+                            const float s0 = bits_to_float<BF>(pa & 0xFFFFu), m0 = bits_to_float<BF>(pa >> 16);
+                            const float s1 = bits_to_float<BF>(pb & 0xFFFFu), m1 = bits_to_float<BF>(pb >> 16);
+#pragma unroll
+                            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                                for (int c = 0; c < 2; c++) {
+                                    const bool begin = i0 + i == 0;
+                                    sc[r][nt][c] = fmaf(s0, dot[r][i][nt][c], begin ? m0 * qsum[nt][0][c] : fmaf(m0, qsum[nt][i0 + i][c], sc[r][nt][c]));
+                                    sc[r][nt][2 + c] = fmaf(s1, dot[r][i][nt][2 + c], begin ? m1 * qsum[nt][0][c] : fmaf(m1, qsum[nt][i0 + i][c], sc[r][nt][2 + c]));
+                                }
                         }
-                    }
-#pragma unroll
-                    for (int nt = 0; nt < NT; nt++) sc[r][nt][0] = sc[r][nt][1] = sc[r][nt][2] = sc[r][nt][3] = 0.0f;
-#pragma unroll
-                    for (int i = 0; i < NG; i++) {
-                        float dot[NT][4];
-#pragma unroll
-                        for (int nt = 0; nt < NT; nt++) dot[nt][0] = dot[nt][1] = dot[nt][2] = dot[nt][3] = 0.0f;
-#pragma unroll
-                        for (int w = i * G / 32; w < (i + 1) * G / 32; w++) {
-                            const unsigned x = ka[w], y = kb[w], xs = x >> 8, ys = y >> 8;
-#pragma unroll
-                            for (int nt = 0; nt < NT; nt++) {
-                                mma(dot[nt], x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u,
-                                    q[nt][2 * w][0], q[nt][2 * w][1]);
-                                mma(dot[nt], xs & 0x000F000Fu, ys & 0x000F000Fu, xs & 0x00F000F0u, ys & 0x00F000F0u,
-                                    q[nt][2 * w + 1][0], q[nt][2 * w + 1][1]);
-                            }
-                        }
-                        const unsigned pa = ppa[i], pb = ppb[i];
-                        const float s0 = bits_to_float<BF>(pa & 0xFFFFu), m0 = bits_to_float<BF>(pa >> 16);
-                        const float s1 = bits_to_float<BF>(pb & 0xFFFFu), m1 = bits_to_float<BF>(pb >> 16);
-#pragma unroll
-                        for (int nt = 0; nt < NT; nt++) {
-#pragma unroll
-                            for (int c = 0; c < 2; c++) {
-                                sc[r][nt][c] = fmaf(s0, dot[nt][c], fmaf(m0, qsum[nt][i][c], sc[r][nt][c]));
-                                sc[r][nt][2 + c] = fmaf(s1, dot[nt][2 + c], fmaf(m1, qsum[nt][i][c], sc[r][nt][2 + c]));
-                            }
-                        }
-                    }
                 }
                 // ---- hidden scores -inf
                 if (!plain) {
