@@ -232,10 +232,15 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
     }
     const long long grid = total < gridDim.x ? total : gridDim.x;
     if (blockIdx.x >= grid) return;
-    long long u = quotient(total * blockIdx.x, grid);
-    const long long u_end = quotient(total * (blockIdx.x + 1), grid);
+    // What only the ends of an item need stays in shared memory, out of the main loop's registers.
+    __shared__ struct {
+        long long total, grid, u, u_end, before;  // before: units of the sequences before b
+        int b;
+    } s_at;
+    {
+    const long long u = quotient(total * blockIdx.x, grid);
     int b = 0;
-    long long before = 0;  // units of the sequences before b
+    long long before = 0;
     {
         long long x = x0, incl = incl0;
         unsigned hit;
@@ -249,7 +254,8 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
         before += __shfl_sync(0xFFFFFFFFu, incl - x, src);
         b += src;
     }
-
+    if (threadIdx.x == 0) s_at = {total, grid, u, quotient(total * (blockIdx.x + 1), grid), before, b};
+    }
     unsigned *tickets = static_cast<unsigned *>(a.ws);
     float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + a.ticket_bytes);
     constexpr int PF = Partial<D, COLS>::kFloats;
@@ -269,10 +275,16 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
     // tickets are drawn after all its work, with one fence.
     struct Shared {
         int first_cta, count, first, n, kvh, ct;
-    } shared[2];
-    shared[0].first_cta = shared[1].first_cta = -1;
+    };
+    __shared__ Shared s_shared[2];
+    if (threadIdx.x == 0) s_shared[0].first_cta = s_shared[1].first_cta = -1;
+    __syncthreads();
 
-    for (; u < u_end;) {
+    for (;;) {
+        long long u = s_at.u, before = s_at.before;
+        const long long u_end = s_at.u_end;
+        int b = s_at.b;
+        if (u >= u_end) break;
         // ---- the item that unit u belongs to; its first kItemUnits units are only its cost
         Seq s = seq_of(p, a, b, COLS, nullptr);
         long long all = (long long)(s.units + kItemUnits) * s.tiles * p.H;
@@ -289,7 +301,20 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
         const int ua = max(from - kItemUnits, 0), ub = max(to - kItemUnits, 0), its = ub - ua;
         const long long item_u0 = u - from + kItemUnits, item_u1 = u - from + per;  // its units that are work
         u += to - from;
-        if (its == 0) continue;
+        __syncthreads();  // all have read s_at
+        if (threadIdx.x == 0) {
+            s_at.u = u;
+            s_at.b = b;
+            s_at.before = before;
+            if (its > 0 && its < s.units) {
+                const int first_cta = (int)cta_of(item_u0, s_at.total, s_at.grid);
+                s_shared[ua == 0] = {first_cta, (int)cta_of(item_u1 - 1, s_at.total, s_at.grid) - first_cta + 1, s.first, s.n, item % p.H, item / p.H};
+            }
+        }
+        if (its == 0) {
+            __syncthreads();
+            continue;
+        }
         const int kvh = item % p.H, ct = item / p.H;
         const long long pos0 = (long long)p.kv_len[b] - s.n;
         if (lane == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring held accumulators
@@ -439,43 +464,39 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
             const bool plain = okr == 3u && tok >= lo_max && tok + kTile - 1 <= hi_min;
             if (okr != 0u && tok < s.len) {
                 float sc[2][NT][4];
-                unsigned kc[2][2][W], kp[2][2][NG];  // codes and parameters of tokens g, 8 + g of either record
-#pragma unroll
-                for (int r = 0; r < 2; r++)
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        load_words<W>(tile + r * RB + h * 4 * D + lane * (D / 8), kc[r][h]);
-                        load_words<NG>(tile + r * RB + R::kPK + (8 * h + g) * NG * 4, kp[r][h]);
-                    }
-                // Groups two at a time: with both records four chains of matrix instructions, in turn, since each waits
-                // for the one before it in its own chain.
+                // Record by record, two groups at a time: two chains of matrix instructions (each waits for the one before it in
+                // its own chain). All of both records' at once measured the same and took 24 registers more.
                 constexpr int GB = NG < 2 ? NG : 2;
 #pragma unroll
-                for (int i0 = 0; i0 < NG; i0 += GB) {
-                    float dot[2][GB][NT][4];
+                for (int r = 0; r < 2; r++) {
+                    unsigned kc[2][W], kp[2][NG];  // codes and parameters of tokens g, 8 + g
 #pragma unroll
-                    for (int w = 0; w < G / 32; w++)
+                    for (int h = 0; h < 2; h++) {
+                        load_words<W>(tile + r * RB + h * 4 * D + lane * (D / 8), kc[h]);
+                        load_words<NG>(tile + r * RB + R::kPK + (8 * h + g) * NG * 4, kp[h]);
+                    }
 #pragma unroll
-                        for (int half = 0; half < 2; half++)
+                    for (int i0 = 0; i0 < NG; i0 += GB) {
+                        float dot[GB][NT][4];
 #pragma unroll
-                            for (int r = 0; r < 2; r++)
+                        for (int w = 0; w < G / 32; w++)
+#pragma unroll
+                            for (int half = 0; half < 2; half++)
 #pragma unroll
                                 for (int i = 0; i < GB; i++) {
                                     const int at = (i0 + i) * G / 32 + w;
-                                    const unsigned x = kc[r][0][at] >> (8 * half), y = kc[r][1][at] >> (8 * half);
+                                    const unsigned x = kc[0][at] >> (8 * half), y = kc[1][at] >> (8 * half);
 #pragma unroll
                                     for (int nt = 0; nt < NT; nt++) {
-                                        float *d = dot[r][i][nt];
+                                        float *d = dot[i][nt];
                                         if (w + half == 0) d[0] = d[1] = d[2] = d[3] = 0.0f;
                                         mma(d, x & 0x000F000Fu, y & 0x000F000Fu, x & 0x00F000F0u, y & 0x00F000F0u,
                                             q[nt][2 * at + half][0], q[nt][2 * at + half][1]);
                                     }
                                 }
 #pragma unroll
-                    for (int r = 0; r < 2; r++)
-#pragma unroll
                         for (int i = 0; i < GB; i++) {
-                            const unsigned pa = kp[r][0][i0 + i], pb = kp[r][1][i0 + i];
+                            const unsigned pa = kp[0][i0 + i], pb = kp[1][i0 + i];
                             const float s0 = bits_to_float<BF>(pa & 0xFFFFu), m0 = bits_to_float<BF>(pa >> 16);
                             const float s1 = bits_to_float<BF>(pb & 0xFFFFu), m1 = bits_to_float<BF>(pb >> 16);
 #pragma unroll
@@ -483,10 +504,11 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
 #pragma unroll
                                 for (int c = 0; c < 2; c++) {
                                     const bool begin = i0 + i == 0;
-                                    sc[r][nt][c] = fmaf(s0, dot[r][i][nt][c], begin ? m0 * qsum[nt][0][c] : fmaf(m0, qsum[nt][i0 + i][c], sc[r][nt][c]));
-                                    sc[r][nt][2 + c] = fmaf(s1, dot[r][i][nt][2 + c], begin ? m1 * qsum[nt][0][c] : fmaf(m1, qsum[nt][i0 + i][c], sc[r][nt][2 + c]));
+                                    sc[r][nt][c] = fmaf(s0, dot[i][nt][c], begin ? m0 * qsum[nt][0][c] : fmaf(m0, qsum[nt][i0 + i][c], sc[r][nt][c]));
+                                    sc[r][nt][2 + c] = fmaf(s1, dot[i][nt][2 + c], begin ? m1 * qsum[nt][0][c] : fmaf(m1, qsum[nt][i0 + i][c], sc[r][nt][2 + c]));
                                 }
                         }
+                    }
                 }
                 // ---- hidden scores -inf
                 if (!plain) {
@@ -726,26 +748,22 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                 }
             }
         }
-        if (!whole) {
-            const int first_cta = (int)cta_of(item_u0, total, grid);
-            shared[ua == 0] = {first_cta, (int)cta_of(item_u1 - 1, total, grid) - first_cta + 1, s.first, s.n, kvh, ct};
-        }
         __syncthreads();  // the ring is free again
     }
 
     // ---- shared items: the last CTA to draw an item's ticket joins its parts, in the order of the ranges. The ticket
     // is that of the item's first CTA, which it is the last item of.
-    if (shared[0].first_cta < 0 && shared[1].first_cta < 0) return;
+    if (s_shared[0].first_cta < 0 && s_shared[1].first_cta < 0) return;
     if (threadIdx.x == 0) {  // after the barrier: what the whole CTA wrote
         __threadfence();
         int last = 0;
 #pragma unroll
         for (int i = 0; i < 2; i++)
-            if (shared[i].first_cta >= 0) {
-                const unsigned was = atomicAdd(tickets + shared[i].first_cta, 1u);
-                if (was == (unsigned)(shared[i].count - 1)) {
+            if (s_shared[i].first_cta >= 0) {
+                const unsigned was = atomicAdd(tickets + s_shared[i].first_cta, 1u);
+                if (was == (unsigned)(s_shared[i].count - 1)) {
                     last |= 1 << i;
-                    tickets[shared[i].first_cta] = 0;
+                    tickets[s_shared[i].first_cta] = 0;
                 }
             }
         __threadfence();
@@ -755,7 +773,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
 #pragma unroll 1
     for (int i = 0; i < 2; i++) {
         if (!((s_last >> i) & 1)) continue;
-        const Shared h = i ? shared[1] : shared[0];
+        const Shared h = s_shared[i];
         const int ncols = min(COLS, h.n * a.R - h.ct * COLS);
         constexpr int L4 = D / 4 < 32 ? D / 4 : 32, PER = D / 4 / L4;  // lanes of a column, groups of 4 channels a lane
         // a warp a column: lane k has part k's maximum and sum, then all lanes add up the parts' channels
