@@ -112,6 +112,7 @@ class Cache4:
         # arguments that every call repeats, as the binding takes them
         self._a = (C.c_void_p(self._pool), self._ref)
         self._shape = (H, D, group)
+        self._tickets = int(self._lib.cg_kv4_ticket_bytes())
         self._fn = {n: getattr(self._lib, "cg_kv4_" + n) for n in ("write", "read", "attention")}
         self._scale = D ** -0.5
 
@@ -127,7 +128,8 @@ class Cache4:
             batch._need[self._shape, Hq] = need
         ws = self._ws.get(stream)
         if ws is None or ws.numel() < need or _capturing():
-            ws = torch.zeros(need, dtype=torch.uint8, device=self._at)
+            ws = torch.empty(need, dtype=torch.uint8, device=self._at)
+            ws[:self._tickets].zero_()
             if not _capturing():
                 self._ws[stream] = ws
         return ws
