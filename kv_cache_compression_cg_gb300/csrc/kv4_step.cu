@@ -136,6 +136,7 @@ struct Seq {
     int len;           // tokens
     int u0, units;     // first unit of 128 tokens that some row sees, and how many
     int tiles;         // column tiles
+    long long pos0;    // position of the first row; may be negative
 };
 __device__ __forceinline__ Seq seq_of(const Kv4 &p, const Kv4Attend &a, int b, int cols, int32_t *status) {
     Seq s;
@@ -145,8 +146,9 @@ __device__ __forceinline__ Seq seq_of(const Kv4 &p, const Kv4Attend &a, int b, i
     s.u0 = 0;
     s.units = 0;
     s.tiles = 0;
+    s.pos0 = 0;
     if (s.n) {
-        const long long pos0 = (long long)p.kv_len[b] - s.n;  // of the first row; may be negative
+        const long long pos0 = s.pos0 = (long long)p.kv_len[b] - s.n;
         const long long lo = a.window && pos0 + 1 > a.window ? pos0 + 1 - a.window : 0;
         s.u0 = (int)((lo < s.len ? lo : s.len) / kUnit);
         const int u1 = (s.len + kUnit - 1) / kUnit;
@@ -208,9 +210,9 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
 
     // ---- the total of all sequences' units, then the sequence that this CTA's range starts in: by every warp for itself,
     // 32 sequences at a time (a barrier would cost more than the repeated loads)
-    auto units = [&](int b0, int32_t *status) -> long long {
+    auto units = [&](int b0, int32_t *status, Seq &s) -> long long {
         if (b0 + lane >= p.B) return 0;
-        const Seq s = seq_of(p, a, b0 + lane, COLS, status);
+        s = seq_of(p, a, b0 + lane, COLS, status);
         return (long long)(s.units + kItemUnits) * s.tiles * p.H;
     };
     auto upto = [&](long long x) {
@@ -221,11 +223,12 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
         }
         return x;
     };
-    const long long x0 = units(0, a.status), incl0 = upto(x0);
+    Seq seq0{}, other;
+    const long long x0 = units(0, a.status, seq0), incl0 = upto(x0);
     long long total = __shfl_sync(0xFFFFFFFFu, incl0, 31);
     if (p.B > 32) {
         long long more = 0;
-        for (int b0 = 32; b0 < p.B; b0 += 32) more += units(b0, a.status);
+        for (int b0 = 32; b0 < p.B; b0 += 32) more += units(b0, a.status, other);
 #pragma unroll
         for (int o = 16; o; o >>= 1) more += __shfl_xor_sync(0xFFFFFFFFu, more, o);
         total += more;
@@ -236,6 +239,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
     __shared__ struct {
         long long total, grid, u, u_end, before;  // before: units of the sequences before b
         int b;
+        Seq s;
     } s_at;
     {
     const long long u = quotient(total * blockIdx.x, grid);
@@ -243,19 +247,21 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
     long long before = 0;
     {
         long long x = x0, incl = incl0;
+        Seq mine = seq0;
         unsigned hit;
         while (!(hit = __ballot_sync(0xFFFFFFFFu, before + incl > u))) {
             before += __shfl_sync(0xFFFFFFFFu, incl, 31);
             b += 32;
-            x = units(b, nullptr);
+            x = units(b, nullptr, mine);
             incl = upto(x);
         }
         const int src = __ffs(hit) - 1;
         before += __shfl_sync(0xFFFFFFFFu, incl - x, src);
         b += src;
+        if (warp == 0 && lane == src) s_at = {total, grid, u, quotient(total * (blockIdx.x + 1), grid), before, b, mine};
     }
-    if (threadIdx.x == 0) s_at = {total, grid, u, quotient(total * (blockIdx.x + 1), grid), before, b};
     }
+
     unsigned *tickets = static_cast<unsigned *>(a.ws);
     float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + a.ticket_bytes);
     constexpr int PF = Partial<D, COLS>::kFloats;
@@ -286,7 +292,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
         int b = s_at.b;
         if (u >= u_end) break;
         // ---- the item that unit u belongs to; its first kItemUnits units are only its cost
-        Seq s = seq_of(p, a, b, COLS, nullptr);
+        Seq s = s_at.s;
         long long all = (long long)(s.units + kItemUnits) * s.tiles * p.H;
         while (u - before >= all) {
             before += all;
@@ -306,6 +312,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
             s_at.u = u;
             s_at.b = b;
             s_at.before = before;
+            s_at.s = s;
             if (its > 0 && its < s.units) {
                 const int first_cta = (int)cta_of(item_u0, s_at.total, s_at.grid);
                 s_shared[ua == 0] = {first_cta, (int)cta_of(item_u1 - 1, s_at.total, s_at.grid) - first_cta + 1, s.first, s.n, item % p.H, item / p.H};
@@ -316,7 +323,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
             continue;
         }
         const int kvh = item % p.H, ct = item / p.H;
-        const long long pos0 = (long long)p.kv_len[b] - s.n;
+        const long long pos0 = s.pos0;
         if (lane == 0) asm volatile("fence.proxy.async.shared::cta;" ::: "memory");  // the ring held accumulators
 
         // ---- queries (the loads): column n = 8 nt + g of the fragment, channels 16j + 4t + 0..3 of step j
@@ -784,7 +791,17 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
             unsigned bb = 0;
 #pragma unroll
             for (int j = 0; j < PER; j++) x[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+            constexpr int BATCH = 16 / PER;
+            float4 y[BATCH][PER];
+            auto load = [&](int k) {  // parts k .. k + BATCH - 1
+#pragma unroll
+                for (int e = 0; e < BATCH; e++)
+#pragma unroll
+                    for (int j = 0; j < PER; j++)
+                        y[e][j] = __ldcg(reinterpret_cast<const float4 *>(part_of(min(k + e, h.count - 1)) + c * D) + j * L4 + lane % L4);
+            };
             for (int k0 = 0; k0 < h.count; k0 += 32) {
+                load(k0);  // in flight with the maxima and sums
                 float pm = -INFINITY, pl = 0.0f;
                 if (k0 + lane < h.count) {
                     const float *tail = part_of(k0 + lane) + COLS * D + 3 * c;
@@ -797,7 +814,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                 for (int o = 16; o; o >>= 1) nm = fmaxf(nm, __shfl_xor_sync(0xFFFFFFFFu, nm, o));
                 const float base = nm == -INFINITY ? 0.0f : nm;
                 const float f0 = top == -INFINITY && tl == 0.0f ? 0.0f : exp2_approx((top == -INFINITY ? base : top) - base);
-                float f = pm == -INFINITY && pl == 0.0f ? 0.0f : exp2_approx((pm == -INFINITY ? base : pm) - base);
+                const float f = pm == -INFINITY && pl == 0.0f ? 0.0f : exp2_approx((pm == -INFINITY ? base : pm) - base);
                 float sum = pl * f;
 #pragma unroll
                 for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
@@ -807,15 +824,10 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                 for (int j = 0; j < PER; j++) x[j].x *= f0, x[j].y *= f0, x[j].z *= f0, x[j].w *= f0;
                 const int many = min(32, h.count - k0);
 #pragma unroll 1
-                for (int k = 0; k < many; k += 8) {
-                    float4 y[8][PER];
+                for (int k = 0; k < many; k += BATCH) {
+                    if (k) load(k0 + k);
 #pragma unroll
-                    for (int e = 0; e < 8; e++)
-#pragma unroll
-                        for (int j = 0; j < PER; j++)
-                            y[e][j] = __ldcg(reinterpret_cast<const float4 *>(part_of(k0 + min(k + e, many - 1)) + c * D) + j * L4 + lane % L4);
-#pragma unroll
-                    for (int e = 0; e < 8; e++) {
+                    for (int e = 0; e < BATCH; e++) {
                         const float fe = __shfl_sync(0xFFFFFFFFu, f, (k + e) & 31);
                         if (k + e < many && fe != 0.0f) {
 #pragma unroll
