@@ -32,6 +32,43 @@ __device__ __forceinline__ unsigned code_of(float x, float lo, float s) {
     return (unsigned)__float2int_rn(fminf(__fdiv_rn(__fsub_rn(x, lo), s), 15.0f));
 }
 
+// Two binary32 side by side.
+__device__ __forceinline__ uint64_t two(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void split(uint64_t r, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r)); }
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// Eight codes by division: K's order (pair j at nibbles j', j' + 4) or V's. Out of line: the kernels run straight through
+// once a warp, and with this inlined most of their stalls were instruction fetches.
+template <bool BF, bool KEYS>
+__device__ __noinline__ unsigned divided(unsigned a, unsigned b, unsigned c, unsigned d, float lo, float s) {
+    const unsigned x[4] = {a, b, c, d};
+    unsigned w = 0;
+#pragma unroll
+    for (int j = 0; j < 4; j++) {
+        const unsigned u = code_of(bits_to_float<BF>(x[j] & 0xFFFFu), lo, s), v = code_of(bits_to_float<BF>(x[j] >> 16), lo, s);
+        w |= KEYS ? (u << (4 * j)) | (v << (4 * j + 16)) : (u << (8 * j)) | (v << (8 * j + 4));
+    }
+    return w;
+}
+
 // Two 16-bit values side by side: the lesser, the greater of each, NaNs kept.
 template <bool BF>
 __device__ __forceinline__ unsigned min_pair(unsigned a, unsigned b) {
@@ -68,41 +105,34 @@ __device__ __forceinline__ void range_of(const unsigned *x, int from, int to, fl
     hi = bits_to_float<BF>(b & 0xFFFFu);
 }
 
-// The codes of N pairs of one group into words: pair j's go to nibbles nib(j), nib2(j) of word j / 4.
-// rint((x - lo) / s) without a division: y = (x - lo) (1/s) is within 2^-19 of the quotient, so its nearest
-// whole number is the quotient's unless y lies that close to halfway; then (or where s is none, or so small
-// that its own rounding let the quotient pass 15) the eight values of the word are divided.
-template <bool BF, int N, typename Nib, typename Nib2>
-__device__ __forceinline__ void codes_of(const unsigned *x, float lo, float hi, float s, unsigned *words, Nib nib,
-                                         Nib2 nib2) {
-    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: y + kMagic has y's nearest whole number in its last bits
-    const bool plain = s > 1e-30f && hi - lo <= 15.4f * s;  // 1/s far from its own limits
+// The codes of N pairs of one group into words, four pairs each: pair j's to nibbles j, j + 4 (KEYS) or 2j, 2j + 1.
+// The quotient of Z without a division a value: with r = 1/s rounded to nearest and y = d r, y + (d - y s) r is d / s
+// rounded to nearest (Markstein's theorem on the last step of a division by fused multiply-adds). A test for quotients
+// near halfway instead, divided when met, cost 60 us more on a 4096-token prefix: 16-bit inputs lie on a grid, and
+// exact ties are some 0.4% of them. Groups whose s is none, far from one, or so small that its own rounding let the
+// quotient pass 15 are divided. Two values an instruction; codes are put together as numbers (16 c' + c and
+// so on up to 2^16), which keeps them off the integer pipe.
+template <bool BF, bool KEYS, int N>
+__device__ __forceinline__ void codes_of(const unsigned *x, float lo, float hi, float s, unsigned *words) {
+    constexpr float kMagic = 12582912.0f;  // 1.5 * 2^23: y + kMagic, less kMagic, is y's nearest whole number, ties to even
+    const bool plain = s > 1e-30f && s < 1e30f && hi - lo <= 15.4f * s;
     const float r = __fdiv_rn(1.0f, s);
+    const uint64_t r2 = two(r, r), lo2 = two(-lo, -lo), s2 = two(-s, -s), magic2 = two(kMagic, kMagic), back2 = two(-kMagic, -kMagic);
 #pragma unroll
     for (int i = 0; i < N / 4; i++) {
-        unsigned w = 0, sub = 0;
-        float far = 0.0f;
+        float c[4], e[4];
 #pragma unroll
-        for (int j = 0; j < 8; j++) {
-            const unsigned pair = x[4 * i + j / 2];
-            const int at = 4 * (j & 1 ? nib2(j / 2) : nib(j / 2));
-            const float d = __fsub_rn(bits_to_float<BF>(j & 1 ? pair >> 16 : pair & 0xFFFFu), lo);
-            const float n = __fmaf_rn(d, r, kMagic);
-            far = fmaxf(far, fabsf(__fmaf_rn(d, r, __fsub_rn(kMagic, n))));
-            w += __float_as_uint(n) << at;
-            sub += 0x4B400000u << at;
+        for (int j = 0; j < 4; j++) {
+            const unsigned pair = x[4 * i + j];
+            const uint64_t d = add2(two(bits_to_float<BF>(pair & 0xFFFFu), bits_to_float<BF>(pair >> 16)), lo2);
+            const uint64_t y = mul2(d, r2);
+            split(add2(add2(fma2(fma2(y, s2, d), r2, y), magic2), back2), c[j], e[j]);
         }
-        w -= sub;
-        if (!(plain && far <= 0.49999f)) {
-            w = 0;
-#pragma unroll
-            for (int j = 0; j < 8; j++) {
-                const unsigned pair = x[4 * i + j / 2];
-                w |= code_of(bits_to_float<BF>(j & 1 ? pair >> 16 : pair & 0xFFFFu), lo, s)
-                     << (4 * (j & 1 ? nib2(j / 2) : nib(j / 2)));
-            }
-        }
-        words[i] = w;
+        // nibbles 0..3 and 4..7 as numbers, then their bits
+        const float low = KEYS ? fmaf(fmaf(fmaf(c[3], 16.0f, c[2]), 16.0f, c[1]), 16.0f, c[0]) : fmaf(fmaf(fmaf(e[1], 16.0f, c[1]), 16.0f, e[0]), 16.0f, c[0]);
+        const float high = KEYS ? fmaf(fmaf(fmaf(e[3], 16.0f, e[2]), 16.0f, e[1]), 16.0f, e[0]) : fmaf(fmaf(fmaf(e[3], 16.0f, c[3]), 16.0f, e[2]), 16.0f, c[2]);
+        words[i] = __byte_perm(__float_as_uint(low + 8388608.0f), __float_as_uint(high + 8388608.0f), 0x5410);
+        if (!plain) words[i] = divided<BF, KEYS>(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3], lo, s);
     }
 }
 
@@ -160,36 +190,42 @@ __device__ __forceinline__ void load_words(const uint8_t *p, unsigned *w) {
     }
 }
 
-// The warp's unit of work: head fastest, so that the warps of a CTA read
-// neighbouring heads of the same rows.
+// The warp's unit of work: head fastest, so that the warps of a CTA read neighbouring heads of the same rows; the layer is
+// the grid's y.
 struct Unit {
     int tile, head, layer;
 };
-__device__ __forceinline__ Unit unit_of(const Kv4 &p, long long w, int tiles) {
-    Unit u;
-    u.head = (int)(w % p.H);
-    w /= p.H;
-    u.tile = (int)(w % tiles);
-    u.layer = (int)(w / tiles);
-    return u;
+__device__ __forceinline__ bool unit_of(const Kv4 &p, int tiles, Unit &u) {
+    const unsigned w = blockIdx.x * 8 + (threadIdx.x >> 5);
+    u.tile = (int)(w / (unsigned)p.H);
+    u.head = (int)(w - (unsigned)u.tile * p.H);
+    u.layer = blockIdx.y;
+    return u.tile < tiles;
 }
 
-// Record of row r's slot, head h, in layer l of the pool: nullptr where it has
-// none. tok = its place in the record.
+// Offset of the record of row r's slot, head h, in layer l of the pool: -1 where it has none. tok = its place in the record.
 __device__ __forceinline__ long long slot_of(const Kv4 &p, int r, int h, int l, int &tok, bool &mine, int32_t *status) {
     int b;
     long long pos;
     mine = r < p.rows && row_pos(p, r, b, pos, status);
-    if (!mine) return -1;
-    const int page = page_of(p, b, pos, status);
-    if (page < 0) return -1;
-    const int at = (int)(pos % p.P);
-    tok = at % kBlk;
-    return l * p.layer_stride + page * p.page_stride + ((long long)h * (p.P / kBlk) + at / kBlk) * p.record;
+    if (!mine || pos < 0) return -1;
+    // positions past the table (and so past 2^31 / page entries) are refused before the divisions, which are 32-bit
+    if (pos >= (long long)p.max_pages * p.P) {
+        raise_flag(status, CG_FLAG_BATCH);
+        return -1;
+    }
+    const unsigned at = (unsigned)pos, i = at / (unsigned)p.P, in = at - i * (unsigned)p.P;
+    const int page = p.table[(long long)b * p.max_pages + i];
+    if (page < 0 || page >= p.pages) {
+        raise_flag(status, CG_FLAG_BATCH);
+        return -1;
+    }
+    tok = in % kBlk;
+    return l * p.layer_stride + page * p.page_stride + ((long long)h * (p.P / kBlk) + in / kBlk) * p.record;
 }
 
 template <int D, int G, bool BF, bool VEC>
-__global__ void __launch_bounds__(256) k_kv4_write(uint8_t *__restrict__ pool, Kv4 p, int layer, int nlayers, int tiles,
+__global__ void __launch_bounds__(256) k_kv4_write(uint8_t *__restrict__ pool, Kv4 p, int layer, int tiles,
                                                    const uint16_t *__restrict__ k, const uint16_t *__restrict__ v,
                                                    long long krs, long long vrs, long long kls, long long vls,
                                                    int32_t *status) {
@@ -198,10 +234,9 @@ __global__ void __launch_bounds__(256) k_kv4_write(uint8_t *__restrict__ pool, K
     constexpr int N = D / 8;               // channels of a V piece
     constexpr int GP = G / N;              // pieces a group
     static_assert(G >= N, "a piece lies in one group");
-    const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (w >= (long long)tiles * p.H * nlayers) return;
+    Unit u;
+    if (!unit_of(p, tiles, u)) return;
     const int lane = threadIdx.x & 31, t = lane & 3, g = lane & 7;
-    const Unit u = unit_of(p, w, tiles);
     // rows past the end load the last one's values and store nothing: no load waits for the slots
     const int last = p.rows - 1, row = u.tile * 8 + (lane >> 2);
     unsigned x[D / 8], z[2][N / 2];  // pairs
@@ -225,8 +260,7 @@ __global__ void __launch_bounds__(256) k_kv4_write(uint8_t *__restrict__ pool, K
             range_of<BF, G / 8>(y, 1, 4, lo, hi);
             const float s = group_scale<BF>(lo, hi);
             // pair j of a word: channels e = 0, 1 (even j) or 2, 3 of step 2w + j / 2
-            codes_of<BF, G / 8>(y, lo, hi, s, words + i * (G / 32), [](int j) { return 2 * (j >> 1) + (j & 1); },
-                                [](int j) { return 4 + 2 * (j >> 1) + (j & 1); });
+            codes_of<BF, true, G / 8>(y, lo, hi, s, words + i * (G / 32));
             if (s != s) {
                 bad |= at >= 0;
                 lo = s;
@@ -250,7 +284,7 @@ __global__ void __launch_bounds__(256) k_kv4_write(uint8_t *__restrict__ pool, K
         range_of<BF, N / 2>(z[half], 1, GP, lo, hi);
         const float s = group_scale<BF>(lo, hi);
         unsigned words[N / 8];
-        codes_of<BF, N / 2>(z[half], lo, hi, s, words, [](int j) { return 2 * j; }, [](int j) { return 2 * j + 1; });
+        codes_of<BF, false, N / 2>(z[half], lo, hi, s, words);
         if (s != s) {
             bad |= vat >= 0;
             lo = s;
@@ -275,8 +309,15 @@ __device__ __forceinline__ unsigned half_bits(float x) {
     if (x < -most) x = -most;
     return float_to_bits<OUT == 2>(x);
 }
+template <bool BF>
+__device__ __forceinline__ unsigned pack16(float lo, float hi) {
+    unsigned y;
+    if (BF) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
 template <int OUT, bool VEC, int N>
-__device__ __forceinline__ void store_values(void *base, long long at, const float *x) {
+__device__ __forceinline__ void store_values(void *base, long long at, const float *x, bool near) {
     if (OUT == 0) {
         float *p = static_cast<float *>(base) + at;
         if (VEC) {
@@ -292,7 +333,8 @@ __device__ __forceinline__ void store_values(void *base, long long at, const flo
         if (VEC) {
             unsigned w[N / 2];
 #pragma unroll
-            for (int i = 0; i < N / 2; i++) w[i] = half_bits<OUT>(x[2 * i]) | (half_bits<OUT>(x[2 * i + 1]) << 16);
+            for (int i = 0; i < N / 2; i++)
+                w[i] = near ? pack16<OUT == 2>(x[2 * i], x[2 * i + 1]) : half_bits<OUT>(x[2 * i]) | (half_bits<OUT>(x[2 * i + 1]) << 16);
             store_words<N / 2>(reinterpret_cast<uint8_t *>(p), w);
         } else {
 #pragma unroll
@@ -302,21 +344,50 @@ __device__ __forceinline__ void store_values(void *base, long long at, const flo
 }
 
 __device__ __forceinline__ float code_value(unsigned word, int nib, float s, float lo) {
-    // 2^23 + c as bits, less 2^23: no conversion instruction; the product is exact, so one rounding
-    const float c = __uint_as_float(((word >> (4 * nib)) & 15u) | 0x4B000000u) - 8388608.0f;
-    return __fmaf_rn(c, s, lo);
+    return __fmaf_rn((float)((word >> (4 * nib)) & 15u), s, lo);  // the product is exact: one rounding
+}
+
+// Eight values out of line: groups near the types' limits, or not finite.
+struct Eight {
+    float x[8];
+};
+__device__ __noinline__ Eight values_far(unsigned word, float s, float lo) {
+    Eight y;
+#pragma unroll
+    for (int i = 0; i < 8; i++) y.x[i] = code_value(word, i, s, lo);
+    return y;
+}
+
+// The values of a word's eight nibbles, in their order; near: |lo| + 15 s < 60000. Two nibbles a mask: as
+// binary16 they are c 2^-24 (c 2^-20), which a conversion and one binary32 fma turn into c s + lo.
+__device__ __forceinline__ void values_of(unsigned word, float s, float lo, bool near, float *x) {
+    if (near) {
+        const float s0 = s * 16777216.0f, s1 = s * 1048576.0f;
+#pragma unroll
+        for (int h = 0; h < 2; h++) {
+            const unsigned w = word >> (8 * h), a = w & 0x000F000Fu, b = w & 0x00F000F0u;
+            const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&a)), v = __half22float2(*reinterpret_cast<const __half2 *>(&b));
+            x[2 * h] = __fmaf_rn(u.x, s0, lo);
+            x[2 * h + 4] = __fmaf_rn(u.y, s0, lo);
+            x[2 * h + 1] = __fmaf_rn(v.x, s1, lo);
+            x[2 * h + 5] = __fmaf_rn(v.y, s1, lo);
+        }
+    } else {
+        const Eight y = values_far(word, s, lo);
+#pragma unroll
+        for (int i = 0; i < 8; i++) x[i] = y.x[i];
+    }
 }
 
 template <int D, int G, int OUT, bool BF, bool VEC>
-__global__ void __launch_bounds__(256) k_kv4_read(const uint8_t *__restrict__ pool, Kv4 p, int layer, int nlayers,
+__global__ void __launch_bounds__(256) k_kv4_read(const uint8_t *__restrict__ pool, Kv4 p, int layer,
                                                   int tiles, void *ok, void *ov, long long rs, long long ls,
                                                   int32_t *status) {
     using R = Rec<D, G>;
     constexpr int W = D / 32;
-    const long long w = ((long long)blockIdx.x * blockDim.x + threadIdx.x) >> 5;
-    if (w >= (long long)tiles * p.H * nlayers) return;
+    Unit u;
+    if (!unit_of(p, tiles, u)) return;
     const int lane = threadIdx.x & 31;
-    const Unit u = unit_of(p, w, tiles);
     const int row = u.tile * 8 + (lane >> 2), t = lane & 3, g = lane & 7;
     int tok = 0;
     bool mine;
@@ -353,26 +424,28 @@ __global__ void __launch_bounds__(256) k_kv4_read(const uint8_t *__restrict__ po
     if (mine) {
         const long long dst = u.layer * ls + row * rs + (long long)u.head * D + 4 * t;
 #pragma unroll
-        for (int j = 0; j < D / 16; j++) {
-            const unsigned pr = params[16 * j / G];
+        for (int w = 0; w < W; w++) {  // channels 32w + 4t + 0..3 and 16 more on: nibbles 0 4 1 5, 2 6 3 7
+            const unsigned pr = params[32 * w / G];
             const float s = bits_to_float<BF>(pr & 0xFFFFu), lo = bits_to_float<BF>(pr >> 16);
-            float x[4];
-#pragma unroll
-            for (int e = 0; e < 4; e++) x[e] = code_value(words[j >> 1], 4 * (e & 1) + 2 * (j & 1) + (e >> 1), s, lo);
-            store_values<OUT, VEC, 4>(ok, dst + 16 * j, x);
+            const bool near = fmaf(15.0f, s, fabsf(lo)) < 60000.0f;
+            float x[8];
+            values_of(words[w], s, lo, near, x);
+            const float y[4] = {x[0], x[4], x[1], x[5]}, z[4] = {x[2], x[6], x[3], x[7]};
+            store_values<OUT, VEC, 4>(ok, dst + 32 * w, y, near);
+            store_values<OUT, VEC, 4>(ok, dst + 32 * w + 16, z, near);
         }
     }
 #pragma unroll
     for (int half = 0; half < 2; half++) {
         if (!vmine[half]) continue;
         const float s = bits_to_float<BF>(vp[half] & 0xFFFFu), lo = bits_to_float<BF>(vp[half] >> 16);
+        const bool near = fmaf(15.0f, s, fabsf(lo)) < 60000.0f;
         const long long dst = u.layer * ls + (u.tile * 8 + half * 4 + (lane >> 3)) * rs + (long long)u.head * D + g * N;
 #pragma unroll
         for (int i = 0; i < N; i += 8) {
             float x[8];
-#pragma unroll
-            for (int j = 0; j < 8; j++) x[j] = code_value(vw[half][i / 8], j, s, lo);
-            store_values<OUT, VEC, 8>(ov, dst + i, x);
+            values_of(vw[half][i / 8], s, lo, near, x);
+            store_values<OUT, VEC, 8>(ov, dst + i, x, near);
         }
     }
 }
@@ -384,10 +457,10 @@ cudaError_t write_dg(uint8_t *pool, const Kv4 &p, int layer, int nl, const void 
                      long long vrs, long long kls, long long vls, int32_t *status, cudaStream_t s) {
     const uint16_t *k = static_cast<const uint16_t *>(kv), *v = static_cast<const uint16_t *>(vv);
     const int tiles = (p.rows + 7) / 8;
-    const unsigned blocks = (unsigned)(((long long)tiles * p.H * nl + 7) / 8);
+    const dim3 blocks((unsigned)(((long long)tiles * p.H + 7) / 8), (unsigned)nl);
     const bool vec = multiple(k, 16) && multiple(v, 16) && krs % 8 == 0 && vrs % 8 == 0 && kls % 8 == 0 && vls % 8 == 0;
 #define CG_KV4_GO(BF, VEC) \
-    k_kv4_write<D, G, BF, VEC><<<blocks, 256, 0, s>>>(pool, p, layer, nl, tiles, k, v, krs, vrs, kls, vls, status)
+    k_kv4_write<D, G, BF, VEC><<<blocks, 256, 0, s>>>(pool, p, layer, tiles, k, v, krs, vrs, kls, vls, status)
     if (p.dtype == CG_DT_BF16) vec ? CG_KV4_GO(true, true) : CG_KV4_GO(true, false);
     else vec ? CG_KV4_GO(false, true) : CG_KV4_GO(false, false);
 #undef CG_KV4_GO
@@ -398,11 +471,11 @@ template <int D, int G>
 cudaError_t read_dg(const uint8_t *pool, const Kv4 &p, int layer, int nl, bool f32, void *ok, void *ov, long long rs,
                     long long ls, int32_t *status, cudaStream_t s) {
     const int tiles = (p.rows + 7) / 8;
-    const unsigned blocks = (unsigned)(((long long)tiles * p.H * nl + 7) / 8);
+    const dim3 blocks((unsigned)(((long long)tiles * p.H + 7) / 8), (unsigned)nl);
     const bool vec = multiple(ok, 16) && multiple(ov, 16) && rs % (f32 ? 4 : 8) == 0 && ls % (f32 ? 4 : 8) == 0;
     const bool bf = p.dtype == CG_DT_BF16;
 #define CG_KV4_GO(OUT, BF, VEC) \
-    k_kv4_read<D, G, OUT, BF, VEC><<<blocks, 256, 0, s>>>(pool, p, layer, nl, tiles, ok, ov, rs, ls, status)
+    k_kv4_read<D, G, OUT, BF, VEC><<<blocks, 256, 0, s>>>(pool, p, layer, tiles, ok, ov, rs, ls, status)
     if (f32) {
         if (bf) vec ? CG_KV4_GO(0, true, true) : CG_KV4_GO(0, true, false);
         else vec ? CG_KV4_GO(0, false, true) : CG_KV4_GO(0, false, false);
