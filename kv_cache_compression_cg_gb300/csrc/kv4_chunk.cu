@@ -9,8 +9,11 @@
 //   16         issues the matrix instructions
 //   17         finds the work
 // Registers go where they are needed (setmaxnreg): 152 a softmax thread, which holds its row's 128 scores.
-// While one tile's softmax runs the tensor cores work for the other one:
-//   ... P0 V, Q0 K', P1 V, Q1 K', ...
+// Tensor memory holds one S, which both row tiles use in turn (a softmax takes its row's 128 scores into registers at
+// once and gives S back), P and O of either. The tensor cores work one key tile ahead of the softmax:
+//   ... Q0 K'(j+1), P0 V(j), Q1 K'(j+1), P1 V(j), ...
+// so a softmax has the time of all four products, not of the other row tile's two (as with an S each, where P has to take
+// its own S's place: 1.85 ms against this one's 1.5 at 4096 rows over 32768 tokens).
 // Rounding. K goes in as s c, exact in binary16 (seven bits times four) under a power of two of the tile; the
 // minima enter as 16 more channels: m_g against the sum of the row's q over the group, that sum as
 // a high and a low part. So scores are exact up to binary32 sums. V goes in as c s + m with one rounding
@@ -285,7 +288,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     using R = Rec<D, G>;
     using S = Smem<D>;
     constexpr int NG = R::NG, W = D / 32, NB = D / 64;
-    constexpr int kS0 = 0, kO0 = 256;  // columns of tensor memory: S of either tile 128, O of either D
+    constexpr int kP0 = kKT, kO0 = 256;  // columns of tensor memory: S 0.. (128), P of either tile (64), O of either (D)
     constexpr int M = 8 / NB;          // pieces of V a block of 64 channels
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[16];
@@ -301,7 +304,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     const unsigned smb = saddr(sm);
     const unsigned bb = saddr(bars);
     const unsigned k_full = bb, k_empty = bb + 16, v_full = bb + 32, v_empty = bb + 48, s_full = bb + 64, p_full = bb + 80,
-                   o_done = bb + 96;  // two of each
+                   o_done = bb + 96, s_free = bb + 112;  // two of each, one s_free
 
     // ---- how much work there is
     long long sum = 0;
@@ -320,6 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             bar_init(p_full + 8 * i, 128);
             bar_init(o_done + 8 * i, 1);
         }
+        bar_init(s_free, 128);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -351,6 +355,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     if (warp == 16) {
         regs_less<kRegsRest>();
         // ---- matrix instructions
+        unsigned n_s = 0;  // turns of S
         for (unsigned round = 0;; round++) {
             __syncthreads();  // (b)
             const Segment &s_seg = s_segs[round & 1];
@@ -359,48 +364,47 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             const bool two = __shfl_sync(0xFFFFFFFFu, s_seg.n * a.R - s_seg.row0 > 128, 0);
             __syncthreads();  // (c)
             constexpr unsigned id_s = idesc_f16(kKT, false), id_o = idesc_f16(D, true);
+            // S is free once the softmax before has it in registers: its turn number n_s
             auto scores = [&](int i, unsigned kv) {
-                const unsigned st = kv & 1, d = tmem + kS0 + i * kKT;
-                const unsigned qa = lo128(smb + S::kQ + i * S::kQTile, 16), ka = lo128(smb + S::kK + st * S::kKStage, 16);
-                mma_scores<0, D>(d, qa, ka, id_s);
-                mma_ss<0, 0>(d, lo_narrow(smb + S::kQN + i * 4096), lo_narrow(smb + S::kKN + st * 4096), kHiNarrow, id_s, true);
-                mma_commit(s_full + 8 * i);
+                if (n_s > 0) wait(s_free, (n_s - 1) & 1);
+                n_s++;
+                fence_after();
+                if (elected()) {
+                    const unsigned st = kv & 1;
+                    mma_scores<0, D>(tmem, lo128(smb + S::kQ + i * S::kQTile, 16), lo128(smb + S::kK + st * S::kKStage, 16), id_s);
+                    mma_ss<0, 0>(tmem, lo_narrow(smb + S::kQN + i * 4096), lo_narrow(smb + S::kKN + st * 4096), kHiNarrow, id_s, true);
+                    mma_commit(s_full + 8 * i);
+                    if (i == 1 || !two) mma_commit(k_empty + 8 * st);
+                }
+                __syncwarp();
+            };
+            auto values = [&](int i, unsigned kv, bool add, unsigned par) {
+                wait(p_full + 8 * i, par);
+                fence_after();
+                if (elected()) {
+                    const unsigned st = kv & 1;
+                    mma_values<0>(tmem + kO0 + i * D, tmem + kP0 + i * (kKT / 2), lo128(smb + S::kV + st * S::kKStage, 16384), id_o, add);
+                    mma_commit(o_done + 8 * i);
+                    if (i == 1 || !two) mma_commit(v_empty + 8 * st);
+                }
+                __syncwarp();
             };
             unsigned kv = n_kv;
             wait(k_full + 8 * (kv & 1), (kv >> 1) & 1);
-            fence_after();
-            if (elected()) {
-                scores(0, kv);
-                if (two) scores(1, kv);
-                mma_commit(k_empty + 8 * (kv & 1));
-            }
-            __syncwarp();
-            auto turn = [&](int i, int j, unsigned parity, bool last) {
-                wait(p_full + 8 * i, parity);
-                fence_after();
-                const unsigned st = kv & 1;
-                if (elected()) {
-                    mma_values<0>(tmem + kO0 + i * D, tmem + kS0 + i * kKT, lo128(smb + S::kV + st * S::kKStage, 16384), id_o, j > 0);
-                    mma_commit(o_done + 8 * i);
-                    if (last) mma_commit(v_empty + 8 * st);
-                }
-                __syncwarp();
-                if (j + 1 < n_tiles) {
-                    if (i == 0) {
-                        wait(k_full + 8 * (st ^ 1), ((kv + 1) >> 1) & 1);
-                        fence_after();
-                    }
-                    if (elected()) {
-                        scores(i, kv + 1);
-                        if (last) mma_commit(k_empty + 8 * (st ^ 1));
-                    }
-                    __syncwarp();
-                }
-            };
+            scores(0, kv);
+            if (two) scores(1, kv);
             for (int j = 0; j < n_tiles; j++, kv++) {
+                const bool ahead = j + 1 < n_tiles;
+                if (ahead) {
+                    wait(k_full + 8 * ((kv + 1) & 1), ((kv + 1) >> 1) & 1);
+                    scores(0, kv + 1);
+                }
                 wait(v_full + 8 * (kv & 1), (kv >> 1) & 1);
-                turn(0, j, (n_q0 + j) & 1, !two);
-                if (two) turn(1, j, (n_q1 + j) & 1, true);
+                values(0, kv, j > 0, (n_q0 + j) & 1);
+                if (two) {
+                    if (ahead) scores(1, kv + 1);
+                    values(1, kv, j > 0, (n_q1 + j) & 1);
+                }
             }
             __syncwarp();
             n_kv += n_tiles;
@@ -744,7 +748,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     } else {
         regs_more<kRegsSoftmax>();
         const int q = warp >> 2, r = threadIdx.x & 127;  // row tile, row
-        const unsigned ts = tmem + kS0 + q * kKT + ((unsigned)(warp & 3) << 21), to = tmem + kO0 + q * D + ((unsigned)(warp & 3) << 21);
+        const unsigned lanes = (unsigned)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
+        const unsigned ts = tmem + lanes, tp = tmem + kP0 + q * (kKT / 2) + lanes, to = tmem + kO0 + q * D + lanes;
         float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + a.ticket_bytes);
         unsigned n_q = 0;
         for (unsigned round = 0;; round++) {
@@ -840,6 +845,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                     const float f = fmaxf(factor * pow2f(info->ek), 1e-37f);  // never zero: a hidden score's -inf stays -inf
                     const bool plain = valid == 0xFFu && tok >= lo_w && tok + kKT - 1 <= hi_w;
                     ld_wait();
+                    fence_before();
+                    bar_arrive(s_free);
                     if (!plain) {
 #pragma unroll
                         for (int i = 0; i < kKT; i++) {
@@ -853,14 +860,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                     float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     top = top == -INFINITY ? top : top * f;
                     const bool raise = top > m + 8.0f;
+                    if (j > 0) {  // the product before this one has taken P, and O is as it left it
+                        wait(o_done + 8 * q, (n_q + j - 1) & 1);
+                        fence_after();
+                    }
                     if (__any_sync(0xFFFFFFFFu, raise || evj != ev)) {
                         const float nm = raise ? top : m;
                         if (j > 0) {
                             const float fm = nm == m ? 1.0f : ex2(m - nm);
                             const float al = fm * (ev - evj < -126 ? 0.0f : pow2f(ev - evj));
                             l *= fm;
-                            wait(o_done + 8 * q, (n_q + j - 1) & 1);
-                            fence_after();
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
                                 unsigned y[16];
@@ -897,7 +906,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                             acc[i & 1] = add_pair(acc[i & 1], pair_of(e0, e1));
                             y[i] = pack_half(e0, e1);
                         }
-                        tmem_st16(ts + 16 * c, y);
+                        tmem_st16(tp + 16 * c, y);
                     }
                     float a0, a1;
                     split(add_pair(acc[0], acc[1]), a0, a1);
