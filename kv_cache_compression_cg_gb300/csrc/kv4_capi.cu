@@ -74,7 +74,7 @@ struct Plan {
 };
 Plan plan_of(const Kv4 &p, int R) {
     Plan plan;
-    plan.chunk = p.D < 256 && (long long)p.max_rows * R > kStepCols;
+    plan.chunk = (long long)p.max_rows * R > kStepCols;
     plan.step = !plan.chunk || (long long)p.rows * R <= (long long)p.B * kStepCols;
     return plan;
 }

@@ -2,9 +2,9 @@
 // include/cachegen.h): prompts and their chunks, on tcgen05.
 //
 // A work item is 256 rows (two tiles of 128; a row is a (row of the batch, query head) pair that shares the KV
-// head) against the key tiles of 128 tokens that they see. Warps of a CTA:
+// head) against the key tiles of 128 tokens that they see (Size has other sizes for 256 channels). Warps of a CTA:
 //   0-3, 4-7   softmax of either row tile: a thread owns a row, that is a lane of tensor memory
-//   8-15       K and V: a record a warp, codes and parameters from the pool to registers (ahead), to binary16
+//   8-15       K and V: a record a warp (or half of one), codes and parameters from the pool to registers (ahead), to binary16
 //              in shared memory, two stages
 //   16         issues the matrix instructions
 //   17         finds the work
@@ -27,8 +27,15 @@
 namespace cg {
 namespace {
 
-constexpr int kKT = 128;          // keys a tile
-constexpr int kRows = 256;        // rows an item
+// Sizes by the channels of a head. 256 channels leave room for one row tile and key tiles of 64: shared memory holds
+// Q (128 x D), two stages of K and of V, tensor memory S, P and O (128 x D binary32 a row tile).
+template <int D>
+struct Size {
+    static constexpr int KT = D == 256 ? 64 : 128;  // keys a tile
+    static constexpr int QT = D == 256 ? 1 : 2;     // row tiles of 128
+    static constexpr int ROWS = 128 * QT;           // rows an item
+    static constexpr int HALVES = KT / 64;          // halves of a record (8 tokens) a warp of 8 has of a tile
+};
 constexpr int kThreads = 20 * 32;
 constexpr int kRegsSoftmax = 152, kRegsStore = 72, kRegsRest = 32;  // x 256, 256, 128 threads: the launch's 640 x 96
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
@@ -90,17 +97,17 @@ __device__ __forceinline__ void mma_ts(unsigned d, unsigned a, unsigned b, unsig
         "r"(a), "r"(b), "r"(hi), "r"(idesc), "r"((unsigned)add), "n"(kOffA), "n"(kOffB)
         : "memory");
 }
-// S = Q K' over D channels; O (+)= P V over 128 keys.
-template <int K, int D>
+// S = Q K' over D channels; O (+)= P V over a tile's keys.
+template <int K, int D, int KT>
 __device__ __forceinline__ void mma_scores(unsigned d, unsigned a, unsigned b, unsigned idesc) {
-    constexpr int off = ((K / 4) * 16384 + (K % 4) * 32) >> 4;
-    mma_ss<off, off>(d, a, b, kHi128, idesc, K > 0);
-    if constexpr (K + 1 < D / 16) mma_scores<K + 1, D>(d, a, b, idesc);
+    constexpr int qo = ((K / 4) * 16384 + (K % 4) * 32) / 16, ko = ((K / 4) * KT * 128 + (K % 4) * 32) / 16;
+    mma_ss<qo, ko>(d, a, b, kHi128, idesc, K > 0);
+    if constexpr (K + 1 < D / 16) mma_scores<K + 1, D, KT>(d, a, b, idesc);
 }
-template <int K>
+template <int K, int KT>
 __device__ __forceinline__ void mma_values(unsigned d, unsigned a, unsigned b, unsigned idesc, bool add) {
     mma_ts<8 * K, K * (2048 >> 4)>(d, a, b, kHi128, idesc, add || K > 0);
-    if constexpr (K + 1 < kKT / 16) mma_values<K + 1>(d, a, b, idesc, add);
+    if constexpr (K + 1 < KT / 16) mma_values<K + 1, KT>(d, a, b, idesc, add);
 }
 __device__ __forceinline__ void mma_commit(unsigned bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
@@ -183,26 +190,32 @@ __device__ __forceinline__ unsigned fma_half(unsigned a, unsigned b, unsigned c)
     asm("fma.rn.f16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(a), "r"(b), "r"(c));
     return y;
 }
+__device__ __forceinline__ unsigned mul_half(unsigned a, unsigned b) {
+    unsigned y;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(y) : "r"(a), "r"(b));
+    return y;
+}
 __device__ __forceinline__ float pow2f(int e) { return __int_as_float((e + 127) << 23); }
 
 // ---- shared memory ----------------------------------------------------------
 template <int D>
 struct Smem {
-    static constexpr int kQ = 0;                         // [tile][D/64][128 rows x 128 bytes]
+    static constexpr int KT = Size<D>::KT, QT = Size<D>::QT;
+    static constexpr int kQ = 0;                           // [tile][D/64][128 rows x 128 bytes]
     static constexpr int kQTile = 128 * D * 2;
-    static constexpr int kK = 2 * kQTile;                // [stage][D/64][128 x 128]
-    static constexpr int kKStage = kKT * D * 2;
-    static constexpr int kV = kK + 2 * kKStage;          // [stage][D/64][128 tokens x 128]
-    static constexpr int kQN = kV + 2 * kKStage;         // narrow: [tile][128 x 16]
-    static constexpr int kKN = kQN + 2 * 4096;           // [stage][128 x 16]
-    static constexpr int kBytes = kKN + 2 * 4096 + 1024; // and the alignment of the first
+    static constexpr int kK = QT * kQTile;                 // [stage][D/64][KT rows x 128 bytes]
+    static constexpr int kStage = KT * D * 2;
+    static constexpr int kV = kK + 2 * kStage;             // [stage][D/64][KT tokens x 128 bytes]
+    static constexpr int kQN = kV + 2 * kStage;            // narrow: [tile][128 x 16]
+    static constexpr int kKN = kQN + QT * 4096;            // [stage][KT x 16]
+    static constexpr int kBytes = kKN + 2 * KT * 32 + 1024;  // and the alignment of the first
 };
 
 struct Info {
-    int ek, ev;       // powers of two of the tile's K and V
-    unsigned valid;   // records that have a page
-    unsigned odd;     // some value group is not finite
+    int ek, ev;     // powers of two of the tile's K and V
+    uint64_t held;  // a byte a warp that stores: 1 if its tokens have a page, 2 if one of their value groups is not finite
 };
+constexpr uint64_t kAllHeld = 0x0101010101010101ull, kSomeOdd = 0x0202020202020202ull;
 
 struct Segment {
     int more;                 // 0: no work is left
@@ -227,29 +240,31 @@ __device__ __forceinline__ Span span_of(const Kv4 &p, const Kv4Attend &a, int b,
     s.pos0 = (long long)p.kv_len[b] - s.n;
     return s;
 }
+template <int D>
 __device__ __forceinline__ void tiles_of(const Span &s, const Kv4Attend &a, int pair, int &t0, int &tiles) {
-    const int last_row = min((pair + 1) * kRows, s.n * a.R) - 1;
-    const long long hi = s.pos0 + last_row / a.R, lo = s.pos0 + (long long)pair * kRows / a.R;
+    const int last_row = min((pair + 1) * Size<D>::ROWS, s.n * a.R) - 1;
+    const long long hi = s.pos0 + last_row / a.R, lo = s.pos0 + (long long)pair * Size<D>::ROWS / a.R;
     const long long end = hi < s.len ? hi + 1 : s.len;  // keys before it are seen by some row
     const long long begin = a.window && lo + 1 > a.window ? lo + 1 - a.window : 0;
     t0 = 0;
     tiles = 1;  // a pair without keys still has outputs
     if (end > begin) {
-        t0 = (int)(begin / kKT);
-        tiles = (int)((end + kKT - 1) / kKT) - t0;
+        t0 = (int)(begin / Size<D>::KT);
+        tiles = (int)((end + Size<D>::KT - 1) / Size<D>::KT) - t0;
     }
 }
 // Units (key tiles of all pairs, over the KV heads) of sequence b0 + lane. Called by a whole warp; sequences of many
 // pairs are summed by all lanes together.
+template <int D>
 __device__ __forceinline__ long long units_of_group(const Kv4 &p, const Kv4Attend &a, int b0, int lane, int32_t *status) {
     Span s{0, 0, 0, 0};
     if (b0 + lane < p.B) s = span_of(p, a, b0 + lane, status);
-    const int pairs = (s.n * a.R + kRows - 1) / kRows;
+    const int pairs = (s.n * a.R + Size<D>::ROWS - 1) / Size<D>::ROWS;
     long long sum = 0;
     int t0, tiles;
     if (__all_sync(0xFFFFFFFFu, pairs <= 4)) {
         for (int i = 0; i < pairs; i++) {
-            tiles_of(s, a, i, t0, tiles);
+            tiles_of<D>(s, a, i, t0, tiles);
             sum += tiles;
         }
     } else {
@@ -263,7 +278,7 @@ __device__ __forceinline__ long long units_of_group(const Kv4 &p, const Kv4Atten
             const int many = __shfl_sync(0xFFFFFFFFu, pairs, src);
             int mine = 0;
             for (int i = lane; i < many; i += 32) {
-                tiles_of(o, a, i, t0, tiles);
+                tiles_of<D>(o, a, i, t0, tiles);
                 mine += tiles;
             }
             mine = __reduce_add_sync(0xFFFFFFFFu, mine);
@@ -279,23 +294,24 @@ __device__ __forceinline__ long long cta_of(long long u, long long total, long l
     return c;
 }
 
-// Partial result of a CTA: [D / 4][256 rows] of 4 accumulators, then maximum, sum and bits of each row.
+// Partial result of a CTA: [D / 4][rows] of 4 accumulators, then maximum, sum and bits of each row.
 template <int D>
-__host__ __device__ constexpr long long partial_floats() { return (long long)kRows * D + 3 * kRows; }
+__host__ __device__ constexpr long long partial_floats() { return (long long)Size<D>::ROWS * (D + 3); }
 
 template <int D, int G, bool BF>
 __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant__ Kv4 p, const __grid_constant__ Kv4Attend a) {
     using R = Rec<D, G>;
     using S = Smem<D>;
     constexpr int NG = R::NG, W = D / 32, NB = D / 64;
-    constexpr int kP0 = kKT, kO0 = 256;  // columns of tensor memory: S 0.. (128), P of either tile (64), O of either (D)
+    constexpr int KT = Size<D>::KT, QT = Size<D>::QT, ROWS = Size<D>::ROWS, HALVES = Size<D>::HALVES;
+    constexpr int kP0 = KT, kO0 = 256;  // columns of tensor memory: S 0.., P of either tile (KT / 2), O of either (D)
     constexpr int M = 8 / NB;          // pieces of V a block of 64 channels
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) uint64_t bars[16];
     __shared__ unsigned s_tmem, s_stop, s_last;
     __shared__ Info s_info[4];
-    __shared__ uint8_t s_odd[4][kKT];  // bits of a token's value groups that are not finite
-    __shared__ float s_emax[2][2][8];
+    __shared__ uint8_t s_odd[4][KT];  // bits of a token's value groups that are not finite
+    __shared__ unsigned s_emax[2][2][8];  // bits of each warp's largest of K, of V
     __shared__ Segment s_segs[2];
     __shared__ long long s_sum[kThreads / 32];
 
@@ -308,7 +324,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
 
     // ---- how much work there is
     long long sum = 0;
-    for (int b0 = warp * 32; b0 < p.B; b0 += kThreads) sum += units_of_group(p, a, b0, lane, a.status);
+    for (int b0 = warp * 32; b0 < p.B; b0 += kThreads) sum += units_of_group<D>(p, a, b0, lane, a.status);
 #pragma unroll
     for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
     if (lane == 0) s_sum[warp] = sum;
@@ -361,9 +377,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             const Segment &s_seg = s_segs[round & 1];
             if (!s_seg.more) break;
             const int n_tiles = __shfl_sync(0xFFFFFFFFu, s_seg.tiles, 0);
-            const bool two = __shfl_sync(0xFFFFFFFFu, s_seg.n * a.R - s_seg.row0 > 128, 0);
+            const bool two = QT == 2 && __shfl_sync(0xFFFFFFFFu, s_seg.n * a.R - s_seg.row0 > 128, 0);
             __syncthreads();  // (c)
-            constexpr unsigned id_s = idesc_f16(kKT, false), id_o = idesc_f16(D, true);
+            constexpr unsigned id_s = idesc_f16(KT, false), id_o = idesc_f16(D, true);
             // S is free once the softmax before has it in registers: its turn number n_s
             auto scores = [&](int i, unsigned kv) {
                 if (n_s > 0) wait(s_free, (n_s - 1) & 1);
@@ -371,8 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                 fence_after();
                 if (elected()) {
                     const unsigned st = kv & 1;
-                    mma_scores<0, D>(tmem, lo128(smb + S::kQ + i * S::kQTile, 16), lo128(smb + S::kK + st * S::kKStage, 16), id_s);
-                    mma_ss<0, 0>(tmem, lo_narrow(smb + S::kQN + i * 4096), lo_narrow(smb + S::kKN + st * 4096), kHiNarrow, id_s, true);
+                    mma_scores<0, D, KT>(tmem, lo128(smb + S::kQ + i * S::kQTile, 16), lo128(smb + S::kK + st * S::kStage, 16), id_s);
+                    mma_ss<0, 0>(tmem, lo_narrow(smb + S::kQN + i * 4096), lo_narrow(smb + S::kKN + st * KT * 32), kHiNarrow, id_s, true);
                     mma_commit(s_full + 8 * i);
                     if (i == 1 || !two) mma_commit(k_empty + 8 * st);
                 }
@@ -383,7 +399,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                 fence_after();
                 if (elected()) {
                     const unsigned st = kv & 1;
-                    mma_values<0>(tmem + kO0 + i * D, tmem + kP0 + i * (kKT / 2), lo128(smb + S::kV + st * S::kKStage, 16384), id_o, add);
+                    mma_values<0, KT>(tmem + kO0 + i * D, tmem + kP0 + i * (KT / 2), lo128(smb + S::kV + st * S::kStage, KT * 128), id_o, add);
                     mma_commit(o_done + 8 * i);
                     if (i == 1 || !two) mma_commit(v_empty + 8 * st);
                 }
@@ -427,7 +443,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
         int b0 = 0, cur = 0;                     // sequences b0.. of this group, the one in work
         long long before = 0, x = 0, incl = 0;   // units before the group; of each lane's sequence; up to its end
         auto group = [&]() {
-            x = units_of_group(p, a, b0, lane, nullptr);
+            x = units_of_group<D>(p, a, b0, lane, nullptr);
             incl = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -452,9 +468,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             int rest = (int)((u - begin) % per);
             int t0 = 0, tiles = 0, pair = 0;
             for (;; pair += 32) {  // 32 pairs at a time
-                const int pairs = (s.n * a.R + kRows - 1) / kRows;
+                const int pairs = (s.n * a.R + ROWS - 1) / ROWS;
                 int mine = 0, from = 0;
-                if (pair + lane < pairs) tiles_of(s, a, pair + lane, from, mine);
+                if (pair + lane < pairs) tiles_of<D>(s, a, pair + lane, from, mine);
                 int upto = mine;
 #pragma unroll
                 for (int o = 1; o < 32; o <<= 1) {
@@ -477,7 +493,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             if (lane == 0) {
                 g.b = b0 + cur;
                 g.kvh = (int)((u - begin) / per);
-                g.row0 = pair * kRows;
+                g.row0 = pair * ROWS;
                 g.first = s.first;
                 g.n = s.n;
                 g.len = s.len;
@@ -519,8 +535,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
         }
     } else if (warp >= 8) {
         regs_less<kRegsStore>();
-        // ---- K and V of the tiles: warp w has record w of each; lanes as in the step kernel
+        // ---- K and V of the tiles: warp w has record w of each (halves h of 8 tokens), or half w % 2 of record w / 2; lanes
+        // as in the step kernel
         const int w = warp - 8, gl = lane >> 2, t = lane & 3, gv = gl * (D / 8) / G;
+        const int tok0 = w * 8 * HALVES, h0 = HALVES == 2 ? 0 : w & 1;  // the warp's first token of a tile; its first half
         const int rpp = p.P / kBlk;
         for (unsigned round = 0;; round++) {
             __syncthreads();  // (b)
@@ -530,154 +548,160 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             const int *table = p.table + (long long)s_seg.b * p.max_pages;
             const uint8_t *heads = a.pool + (long long)s_seg.kvh * rpp * R::kBytes;
             __syncthreads();  // (c)
-            auto page_at = [&](int j) {  // page of the warp's record of tile j
-                int pg = -1;
-                const long long tok = (long long)(tile0 + j) * kKT + w * kBlk;
-                if (j < n_tiles && tok < len) {
-                    pg = __ldg(table + (int)(tok / p.P));
-                    if (pg < 0 || pg >= p.pages) {
-                        if (lane == 0) raise_flag(a.status, CG_FLAG_BATCH);
-                        pg = -1;
+            long long at = -1;  // lane i: offset of the warp's record of tile i of the 32 last looked up, -1 where it has no page
+            auto record = [&](int j) {  // of tile j: called for 0, 1, 2, ...
+                if ((j & 31) == 0) {
+                    const unsigned rec = (unsigned)(tile0 + j + lane) * (KT / kBlk) + tok0 / kBlk;
+                    at = -1;
+                    if (j + lane < n_tiles && (long long)rec * kBlk < len) {
+                        const unsigned i = rec / (unsigned)rpp;
+                        const int page = __ldg(table + i);
+                        if (page < 0 || page >= p.pages) raise_flag(a.status, CG_FLAG_BATCH);
+                        else at = page * p.page_stride + (long long)(rec - i * rpp) * R::kBytes;
                     }
                 }
-                return pg;
+                return __shfl_sync(0xFFFFFFFFu, at, j & 31);
             };
-            auto record = [&](int j, int pg) { return heads + pg * p.page_stride + (long long)(((tile0 + j) * (kKT / kBlk) + w) % rpp) * R::kBytes; };
-            unsigned kr[2][W], vr[2][W], kp[2][NG], vp[2][2];
+            unsigned kr[HALVES][W], vr[HALVES][W], kp[HALVES][NG], vp[HALVES][2];
             auto fetch = [&](unsigned (*x)[W], const uint8_t *src) {
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const uint8_t *c = src + h * 4 * D + lane * (D / 8);
+                for (int h = 0; h < HALVES; h++) {
+                    const uint8_t *c = src + (h0 + h) * 4 * D + lane * (D / 8);
                     if (W == 2) {
                         const uint2 y = __ldg(reinterpret_cast<const uint2 *>(c));
                         x[h][0] = y.x, x[h][1] = y.y;
                     } else {
-                        const uint4 y = __ldg(reinterpret_cast<const uint4 *>(c));
-                        x[h][0] = y.x, x[h][1] = y.y, x[h][2 % W] = y.z, x[h][3 % W] = y.w;
+#pragma unroll
+                        for (int i = 0; i < W; i += 4) {
+                            const uint4 y = __ldg(reinterpret_cast<const uint4 *>(c) + i / 4);
+                            x[h][i] = y.x, x[h][i + 1] = y.y, x[h][(i + 2) % W] = y.z, x[h][(i + 3) % W] = y.w;
+                        }
                     }
                 }
             };
-            auto fetch_params = [&](const uint8_t *src, unsigned (*xk)[NG], unsigned (*xv)[2]) {
+            auto fetch_params = [&](const uint8_t *src) {
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const unsigned *pk = reinterpret_cast<const unsigned *>(src + R::kPK) + (8 * h + gl) * NG;
+                for (int h = 0; h < HALVES; h++) {
+                    const unsigned *pk = reinterpret_cast<const unsigned *>(src + R::kPK) + (8 * (h0 + h) + gl) * NG;
 #pragma unroll
-                    for (int c = 0; c < NG; c++) xk[h][c] = __ldg(pk + c);
-                    const unsigned *pv = reinterpret_cast<const unsigned *>(src + R::kPV) + (8 * h + 2 * t) * NG + gv;
-                    xv[h][0] = __ldg(pv);
-                    xv[h][1] = __ldg(pv + NG);
+                    for (int c = 0; c < NG; c++) kp[h][c] = __ldg(pk + c);
+                    const unsigned *pv = reinterpret_cast<const unsigned *>(src + R::kPV) + (8 * (h0 + h) + 2 * t) * NG + gv;
+                    vp[h][0] = __ldg(pv);
+                    vp[h][1] = __ldg(pv + NG);
                 }
             };
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
+            for (int h = 0; h < HALVES; h++) {
 #pragma unroll
                 for (int c = 0; c < W; c++) kr[h][c] = vr[h][c] = 0;
 #pragma unroll
                 for (int c = 0; c < NG; c++) kp[h][c] = 0;
                 vp[h][0] = vp[h][1] = 0;
             }
-            int pg = page_at(0), pg1 = page_at(1);
-            if (pg >= 0) {
-                const uint8_t *src = record(0, pg);
-                fetch_params(src, kp, vp);
-                fetch(kr, src);
-                fetch(vr, src + R::kV);
+            long long now = record(0);
+            if (now >= 0) {
+                fetch_params(heads + now);
+                fetch(kr, heads + now);
+                fetch(vr, heads + now + R::kV);
             }
             int sig = kSigMin;
             for (int j = 0; j < n_tiles; j++) {
                 const unsigned kv = n_kv + j, st = kv & 1, par = ((kv >> 1) & 1) ^ 1;
-                const int base = (tile0 + j) * kKT + w * kBlk;
-                const uint8_t *src1 = record(j + 1, pg1);
-                const int pg2 = page_at(j + 2);
-                // parameters of tokens that the sequence does not hold count as zero; a value group that is not finite too
-                // (its rows are found by their bits), a key group's NaN stays
-                float kmax = 0.0f, vmax = 0.0f;
-                unsigned odd = 0;
+                const int base = (tile0 + j) * KT + tok0;
+                const long long then = j + 1 < n_tiles ? record(j + 1) : -1;
+                float kmax = 0.0f, vmax = 0.0f, check = 0.0f;
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const bool have = pg >= 0 && base + 8 * h + gl < len;
+                for (int h = 0; h < HALVES; h++) {
 #pragma unroll
-                    for (int c = 0; c < NG; c++) {
-                        if (!have) kp[h][c] = 0;
-                        kmax = fmaxf(kmax, fmaxf(15.0f * bits_to_float<BF>(kp[h][c] & 0xFFFFu), fabsf(bits_to_float<BF>(kp[h][c] >> 16))));
-                    }
+                    for (int c = 0; c < NG; c++)
+                        kmax = max3(kmax, 15.0f * bits_to_float<BF>(kp[h][c] & 0xFFFFu), fabsf(bits_to_float<BF>(kp[h][c] >> 16)));
 #pragma unroll
                     for (int y = 0; y < 2; y++) {
                         const float s = bits_to_float<BF>(vp[h][y] & 0xFFFFu), m = bits_to_float<BF>(vp[h][y] >> 16);
-                        const bool held = pg >= 0 && base + 8 * h + 2 * t + y < len, fine = fabsf(s) <= kMaxF && fabsf(m) <= kMaxF;
-                        if (held && !fine) odd |= 1u << (2 * h + y);
-                        if (!held || !fine) vp[h][y] = 0;
-                        else vmax = fmaxf(vmax, fmaxf(fabsf(m), fabsf(fmaf(15.0f, s, m))));
+                        check = fmaf(s, 0.0f, check);  // NaN where a scale is not finite
+                        vmax = max3(vmax, fabsf(m), fabsf(fmaf(15.0f, s, m)));
                     }
+                }
+                unsigned odd = 0;
+                bool any_odd = false;
+                if (__any_sync(0xFFFFFFFFu, check != 0.0f || now < 0 || base + 8 * HALVES > len)) {
+                    // parameters of tokens that the sequence does not hold count as zero; a value group that is not finite
+                    // too (its rows are found by their bits), a key group's NaN stays
+                    kmax = vmax = 0.0f;
+#pragma unroll
+                    for (int h = 0; h < HALVES; h++) {
+                        const bool have = now >= 0 && base + 8 * h + gl < len;
+#pragma unroll
+                        for (int c = 0; c < NG; c++) {
+                            if (!have) kp[h][c] = 0;
+                            kmax = max3(kmax, 15.0f * bits_to_float<BF>(kp[h][c] & 0xFFFFu), fabsf(bits_to_float<BF>(kp[h][c] >> 16)));
+                        }
+#pragma unroll
+                        for (int y = 0; y < 2; y++) {
+                            const float s = bits_to_float<BF>(vp[h][y] & 0xFFFFu), m = bits_to_float<BF>(vp[h][y] >> 16);
+                            const bool held = now >= 0 && base + 8 * h + 2 * t + y < len, fine = fabsf(s) <= kMaxF && fabsf(m) <= kMaxF;
+                            if (held && !fine) odd |= 1u << (2 * h + y);
+                            if (!held || !fine) vp[h][y] = 0;
+                            else vmax = max3(vmax, fabsf(m), fabsf(fmaf(15.0f, s, m)));
+                        }
+                    }
+                    any_odd = __any_sync(0xFFFFFFFFu, odd != 0);
                 }
                 const unsigned ku = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(kmax, kMaxF)));
                 const unsigned vu = __reduce_max_sync(0xFFFFFFFFu, __float_as_uint(fminf(vmax, kMaxF)));
-                if (lane == 0) {
-                    s_emax[j & 1][0][w] = __uint_as_float(ku);
-                    s_emax[j & 1][1][w] = __uint_as_float(vu);
-                }
-                const unsigned any_odd = __ballot_sync(0xFFFFFFFFu, odd != 0);
                 Info *info = &s_info[kv & 3];
                 // the entry's last readers are done: this tile's K stage is free only after the scores two tiles on
                 wait(k_empty + 8 * st, par);
-                if (w == 0 && lane == 0) {
-                    info->valid = 0;
-                    info->odd = 0;
-                }
-                asm volatile("bar.sync 1, 256;" ::: "memory");
                 if (lane == 0) {
-                    if (pg >= 0) atomicOr(&info->valid, 1u << w);
-                    if (any_odd) atomicOr(&info->odd, 1u << w);
+                    s_emax[j & 1][0][w] = ku;
+                    s_emax[j & 1][1][w] = vu;
+                    reinterpret_cast<uint8_t *>(&info->held)[w] = (uint8_t)((now >= 0 ? 1 : 0) | (any_odd ? 2 : 0));
                 }
                 if (any_odd) {  // rare: bits of each token's groups
 #pragma unroll
-                    for (int h = 0; h < 2; h++)
+                    for (int h = 0; h < HALVES; h++)
 #pragma unroll
                         for (int y = 0; y < 2; y++) {
                             unsigned bits = (odd >> (2 * h + y)) & 1u ? 1u << gv : 0u;  // over the lanes of equal t
                             bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, 4);
                             bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, 8);
                             bits |= __shfl_xor_sync(0xFFFFFFFFu, bits, 16);
-                            if (gl == 0) s_odd[kv & 3][w * kBlk + 8 * h + 2 * t + y] = (uint8_t)bits;
+                            if (gl == 0) s_odd[kv & 3][tok0 + 8 * h + 2 * t + y] = (uint8_t)bits;
                         }
-                } else if (lane < kBlk) {
-                    s_odd[kv & 3][w * kBlk + lane] = 0;
                 }
-                float km = s_emax[j & 1][0][0], vm = s_emax[j & 1][1][0];
-#pragma unroll
-                for (int i = 1; i < 8; i++) {
-                    km = fmaxf(km, s_emax[j & 1][0][i]);
-                    vm = fmaxf(vm, s_emax[j & 1][1][i]);
-                }
+                asm volatile("bar.sync 1, 256;" ::: "memory");
+                const unsigned km = __reduce_max_sync(0xFFFFFFFFu, s_emax[j & 1][0][lane & 7]);
+                const unsigned vm = __reduce_max_sync(0xFFFFFFFFu, s_emax[j & 1][1][lane & 7]);
                 // K: the tile's largest of 15 s and |m| goes to [2^8, 2^9), so 1024 s stays in binary16
-                const int ek = max((int)(__float_as_uint(km) >> 23) - 127, -110) - 8;
-                sig = max(sig, (int)(__float_as_uint(vm) >> 23) - 127);
+                const int ek = max((int)(km >> 23) - 127, -110) - 8;
+                sig = max(sig, (int)(vm >> 23) - 127);
                 if (w == 0 && lane == 0) {
                     info->ek = ek;
                     info->ev = sig;
                 }
                 const float kf = pow2f(-ek);
-                uint8_t *kd = sm + S::kK + st * S::kKStage, *kn = sm + S::kKN + st * 4096;
+                uint8_t *kd = sm + S::kK + st * S::kStage, *kn = sm + S::kKN + st * KT * 32;
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const int row = w * kBlk + 8 * h + gl;
+                for (int h = 0; h < HALVES; h++) {
+                    const int row = tok0 + 8 * h + gl;  // row % 8 == gl
+                    uint8_t *dst = kd + row * 128;
                     unsigned ms[NG];
 #pragma unroll
                     for (int c = 0; c < NG; c++) {
                         const float s = bits_to_float<BF>(kp[h][c] & 0xFFFFu) * kf, m = bits_to_float<BF>(kp[h][c] >> 16) * kf;
                         ms[c] = pack_half(m, m) & 0xFFFFu;
                         const unsigned s1 = pack_half(s, s), s16 = pack_half(s * 0.0625f, s * 0.0625f);
-                        const unsigned z1 = pack_half(s * -1024.0f, s * -1024.0f), z16 = pack_half(s * -64.0f, s * -64.0f);
+                        const unsigned z1 = mul_half(s1, 0xE400E400u), z16 = mul_half(s16, 0xE400E400u);  // times -1024
 #pragma unroll
                         for (int x = c * G / 32; x < (c + 1) * G / 32; x++) {
-                            // 1024 + c and 1024 + 16 c as bits; times s, less 1024 s (64 s): s c, exactly
+                            // 1024 + c and 1024 + 16 c as bits; times s, less 1024 s (s / 16, 64 s): s c, exactly
                             const unsigned u0 = kr[h][x], u1 = u0 >> 8;
                             uint4 y;
                             y.x = fma_half((u0 & 0x000F000Fu) | 0x64006400u, s1, z1);
                             y.y = fma_half((u0 & 0x00F000F0u) | 0x64006400u, s16, z16);
                             y.z = fma_half((u1 & 0x000F000Fu) | 0x64006400u, s1, z1);
                             y.w = fma_half((u1 & 0x00F000F0u) | 0x64006400u, s16, z16);
-                            *reinterpret_cast<uint4 *>(kd + (x >> 1) * 16384 + row * 128 + (((2 * t + (x & 1)) ^ (row & 7)) << 4)) = y;
+                            *reinterpret_cast<uint4 *>(dst + (x >> 1) * (KT * 128) + (((2 * t + (x & 1)) ^ gl) << 4)) = y;
                         }
                     }
                     if (t < 2) {  // minima: channels 0..NG-1 and once more, 8 a lane
@@ -692,35 +716,34 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                             }
                             o8[c] = lo | (hi << 16);
                         }
-                        *reinterpret_cast<uint4 *>(kn + (row >> 3) * 256 + t * 128 + (row & 7) * 16) = make_uint4(o8[0], o8[1], o8[2], o8[3]);
+                        *reinterpret_cast<uint4 *>(kn + (row >> 3) * 256 + t * 128 + gl * 16) = make_uint4(o8[0], o8[1], o8[2], o8[3]);
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 bar_arrive(k_full + 8 * st);
-                const float vf = pow2f(17 - sig);
-                unsigned vs[2][2], vm2[2][2];  // s and m of tokens 2t, 2t + 1 of either half, scaled
+                const float vf = pow2f(17 - sig), vg = vf * 5.9604644775390625e-8f;
+                unsigned vs[HALVES][2], vm2[HALVES][2];  // s and m of tokens 2t, 2t + 1 of either half, scaled
 #pragma unroll
-                for (int h = 0; h < 2; h++)
+                for (int h = 0; h < HALVES; h++)
 #pragma unroll
                     for (int y = 0; y < 2; y++) {
-                        const float s = bits_to_float<BF>(vp[h][y] & 0xFFFFu) * vf;
-                        const float m = bits_to_float<BF>(vp[h][y] >> 16) * 5.9604644775390625e-8f * vf;
-                        vs[h][y] = pack_half(s, s * 0.0625f);
+                        const float s = bits_to_float<BF>(vp[h][y] & 0xFFFFu) * vf, m = bits_to_float<BF>(vp[h][y] >> 16) * vg;
+                        vs[h][y] = pack_half(s, s);
                         vm2[h][y] = pack_half(m, m);
                     }
-                if (pg1 >= 0) {
-                    fetch_params(src1, kp, vp);
-                    fetch(kr, src1);
+                if (then >= 0) {
+                    fetch_params(heads + then);
+                    fetch(kr, heads + then);
                 }
                 wait(v_empty + 8 * st, par);
-                uint8_t *vd = sm + S::kV + st * S::kKStage;
+                uint8_t *vd = sm + S::kV + st * S::kStage + (gl / M) * (KT * 128);
                 constexpr int VW = D / 64;  // words of a token's piece
 #pragma unroll
-                for (int h = 0; h < 2; h++)
+                for (int h = 0; h < HALVES; h++)
 #pragma unroll
                     for (int y = 0; y < 2; y++) {
-                        const int row = w * kBlk + 8 * h + 2 * t + y;
-                        const unsigned s1 = __byte_perm(vs[h][y], 0, 0x1010), s16 = __byte_perm(vs[h][y], 0, 0x3232), mm = vm2[h][y];
+                        const int row = tok0 + 8 * h + 2 * t + y;  // row % 8 == 2t + y
+                        const unsigned s1 = vs[h][y], s16 = mul_half(s1, 0x2C002C00u), mm = vm2[h][y];  // s / 16
 #pragma unroll
                         for (int x = 0; x < VW; x++) {
                             const unsigned u0 = vr[h][y * VW + x], u1 = u0 >> 8;
@@ -729,15 +752,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                             z.y = fma_half(u0 & 0x00F000F0u, s16, mm);
                             z.z = fma_half(u1 & 0x000F000Fu, s1, mm);
                             z.w = fma_half(u1 & 0x00F000F0u, s16, mm);
-                            const int chunk = (gl % M) + M * x;
-                            *reinterpret_cast<uint4 *>(vd + (gl / M) * 16384 + row * 128 + ((chunk ^ (row & 7)) << 4)) = z;
+                            *reinterpret_cast<uint4 *>(vd + row * 128 + ((((gl % M) + M * x) ^ (2 * t + y)) << 4)) = z;
                         }
                     }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 bar_arrive(v_full + 8 * st);
-                if (pg1 >= 0) fetch(vr, src1 + R::kV);
-                pg = pg1;
-                pg1 = pg2;
+                if (then >= 0) fetch(vr, heads + then + R::kV);
+                now = then;
             }
             n_kv += n_tiles;
             if (!s_seg.whole) {
@@ -749,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
         regs_more<kRegsSoftmax>();
         const int q = warp >> 2, r = threadIdx.x & 127;  // row tile, row
         const unsigned lanes = (unsigned)(warp & 3) << 21;  // this warp's 32 lanes of tensor memory
-        const unsigned ts = tmem + lanes, tp = tmem + kP0 + q * (kKT / 2) + lanes, to = tmem + kO0 + q * D + lanes;
+        const unsigned ts = tmem + lanes, tp = tmem + kP0 + q * (KT / 2) + lanes, to = tmem + kO0 + q * D + lanes;
         float *partials = reinterpret_cast<float *>(static_cast<uint8_t *>(a.ws) + a.ticket_bytes);
         unsigned n_q = 0;
         for (unsigned round = 0;; round++) {
@@ -758,13 +779,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             if (!s_seg.more) break;
             const int tile0 = s_seg.tile0, n_tiles = s_seg.tiles, len = s_seg.len;
             const int rho = s_seg.row0 + q * 128 + r;
-            const bool mine = rho < s_seg.n * a.R, active = q == 0 || s_seg.n * a.R - s_seg.row0 > 128;
+            const bool active = q == 0 || (QT == 2 && s_seg.n * a.R - s_seg.row0 > 128), mine = active && rho < s_seg.n * a.R;
             const int irow = rho / a.R, head = s_seg.kvh * a.R + rho % a.R;
             const long long out_row = s_seg.first + irow, pos = s_seg.pos0 + irow;
             float factor = 0.0f;
             // ---- queries: under 2^kq of the row's own; a chunk of 16 bytes holds channels 32w + 4t + 0..3 and
             // 16 more on, w = 2 block + chunk % 2, t = chunk / 2: the order K's chunks come in
-            {
+            if (active) {
                 const uint16_t *src = a.q + out_row * a.q_stride + (long long)head * D;
                 unsigned in[D / 2];  // pairs of channels
                 if (!mine) {
@@ -836,27 +857,27 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                     const unsigned kv = n_kv + j;
                     wait(s_full + 8 * q, (n_q + j) & 1);
                     fence_after();
-                    unsigned x[kKT];
+                    unsigned x[KT];
 #pragma unroll
-                    for (int c = 0; c < 4; c++) tmem_ld32(ts + 32 * c, x + 32 * c);
+                    for (int c = 0; c < KT / 32; c++) tmem_ld32(ts + 32 * c, x + 32 * c);
                     const volatile Info *info = &s_info[kv & 3];
-                    const int tok = (tile0 + j) * kKT, evj = info->ev;
-                    const unsigned valid = info->valid;
+                    const int tok = (tile0 + j) * KT, evj = info->ev;
+                    const uint64_t held = info->held;
                     const float f = fmaxf(factor * pow2f(info->ek), 1e-37f);  // never zero: a hidden score's -inf stays -inf
-                    const bool plain = valid == 0xFFu && tok >= lo_w && tok + kKT - 1 <= hi_w;
+                    const bool plain = (held & kAllHeld) == kAllHeld && tok >= lo_w && tok + KT - 1 <= hi_w;
                     ld_wait();
                     fence_before();
                     bar_arrive(s_free);
                     if (!plain) {
 #pragma unroll
-                        for (int i = 0; i < kKT; i++) {
+                        for (int i = 0; i < KT; i++) {
                             const int at = tok + i;
-                            if (at > hi || at < lo || !((valid >> (i / 16)) & 1u)) x[i] = 0xFF800000u;
+                            if (at > hi || at < lo || !((held >> (8 * (i / (8 * HALVES)))) & 1u)) x[i] = 0xFF800000u;
                         }
                     }
                     float t4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < kKT; i += 2) t4[(i / 2) & 3] = max3(t4[(i / 2) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+                    for (int i = 0; i < KT; i += 2) t4[(i / 2) & 3] = max3(t4[(i / 2) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                     float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     top = top == -INFINITY ? top : top * f;
                     const bool raise = top > m + 8.0f;
@@ -884,18 +905,18 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                         m = nm;
                         ev = evj;
                     }
-                    if (info->odd) {  // rare: which columns' groups are not finite, for the keys this row sees
+                    if (held & kSomeOdd) {  // rare: which columns' groups are not finite, for the keys this row sees
 #pragma unroll 1
-                        for (int c = 0; c < kKT; c++) {
+                        for (int c = 0; c < KT; c++) {
                             const int at = tok + c;
-                            if (mine && at <= hi && at >= lo && ((valid >> (c / 16)) & 1u)) bits |= *(volatile uint8_t *)&s_odd[kv & 3][c];
+                            if (mine && at <= hi && at >= lo && ((held >> (8 * (c / (8 * HALVES)))) & 3u) == 3u) bits |= *(volatile uint8_t *)&s_odd[kv & 3][c];
                         }
                     }
                     const float base = m == -INFINITY ? 0.0f : m;
                     const uint64_t f2 = pair_of(f, f), b2 = pair_of(-base, -base);
                     uint64_t acc[2] = {0, 0};
 #pragma unroll
-                    for (int c = 0; c < 4; c++) {
+                    for (int c = 0; c < KT / 32; c++) {
                         unsigned y[16];
 #pragma unroll
                         for (int i = 0; i < 16; i++) {
@@ -959,17 +980,17 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                     } else {
 #pragma unroll
                         for (int i = 0; i < 8; i++)
-                            *reinterpret_cast<uint4 *>(part + ((long long)(8 * c + i) * kRows + q * 128 + r) * 4) =
+                            *reinterpret_cast<uint4 *>(part + ((long long)(8 * c + i) * ROWS + q * 128 + r) * 4) =
                                 make_uint4(x[4 * i], x[4 * i + 1], x[4 * i + 2], x[4 * i + 3]);
                     }
                 }
                 if (whole) {
                     if (mine && a.lse) a.lse[out_row * a.Hq + head] = l == 0.0f ? -INFINITY : (m == -INFINITY ? 0.0f : m) * kLn2 + logf(l);
                 } else {
-                    float *tail = part + kRows * D + q * 128 + r;
+                    float *tail = part + ROWS * D + q * 128 + r;
                     tail[0] = m;
-                    tail[kRows] = l;
-                    tail[2 * kRows] = __uint_as_float(bits);
+                    tail[ROWS] = l;
+                    tail[2 * ROWS] = __uint_as_float(bits);
                 }
                 fence_before();
                 n_q += n_tiles;
@@ -986,14 +1007,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                 const long long c0 = s_seg.cta0;
                 auto part_of = [&](int k) { return partials + ((c0 + k) * 2 + (k == 0 ? 1 : 0)) * partial_floats<D>(); };
                 float top = -INFINITY;
-                for (int k = 0; k < count; k++) top = fmaxf(top, __ldcg(part_of(k) + kRows * D + at));
+                for (int k = 0; k < count; k++) top = fmaxf(top, __ldcg(part_of(k) + ROWS * D + at));
                 const float base = top == -INFINITY ? 0.0f : top;
                 float l = 0.0f;
                 unsigned bits = 0;
                 for (int k = 0; k < count; k++) {
-                    const float *tail = part_of(k) + kRows * D + at;
-                    l += __ldcg(tail + kRows) * ex2(__ldcg(tail) - base);
-                    bits |= __float_as_uint(__ldcg(tail + 2 * kRows));
+                    const float *tail = part_of(k) + ROWS * D + at;
+                    l += __ldcg(tail + ROWS) * ex2(__ldcg(tail) - base);
+                    bits |= __float_as_uint(__ldcg(tail + 2 * ROWS));
                 }
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 uint16_t *dst = a.out + out_row * a.out_stride + (long long)head * D;
@@ -1004,9 +1025,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                     for (int i = 0; i < 8; i++) x[i] = 0.0f;
                     for (int k = 0; k < count; k++) {
                         const float *src = part_of(k);
-                        const float f = ex2(__ldcg(src + kRows * D + at) - base);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + ((long long)(2 * c8) * kRows + at) * 4));
-                        const float4 z = __ldcg(reinterpret_cast<const float4 *>(src + ((long long)(2 * c8 + 1) * kRows + at) * 4));
+                        const float f = ex2(__ldcg(src + ROWS * D + at) - base);
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + ((long long)(2 * c8) * ROWS + at) * 4));
+                        const float4 z = __ldcg(reinterpret_cast<const float4 *>(src + ((long long)(2 * c8 + 1) * ROWS + at) * 4));
                         x[0] += y.x * f, x[1] += y.y * f, x[2] += y.z * f, x[3] += y.w * f;
                         x[4] += z.x * f, x[5] += z.y * f, x[6] += z.z * f, x[7] += z.w * f;
                     }
@@ -1050,7 +1071,8 @@ cudaError_t chunk_dg(const Kv4 &p, const Kv4Attend &a, cudaStream_t s) {
 }  // namespace
 
 uint64_t kv4_chunk_workspace_bytes(const Kv4 &p) {
-    return kv4_ticket_bytes() + 2ull * kMaxGrid * 4 * ((uint64_t)kRows * p.D + 3 * kRows);
+    const uint64_t rows = p.D == 256 ? Size<256>::ROWS : Size<128>::ROWS;
+    return kv4_ticket_bytes() + 2ull * kMaxGrid * 4 * rows * (p.D + 3);
 }
 
 cudaError_t launch_kv4_chunk(const Kv4 &p, const Kv4Attend &a, cudaStream_t s) {
@@ -1060,6 +1082,9 @@ cudaError_t launch_kv4_chunk(const Kv4 &p, const Kv4Attend &a, cudaStream_t s) {
         case 128032: return chunk_dg<128, 32>(p, a, s);
         case 128064: return chunk_dg<128, 64>(p, a, s);
         case 128128: return chunk_dg<128, 128>(p, a, s);
+        case 256032: return chunk_dg<256, 32>(p, a, s);
+        case 256064: return chunk_dg<256, 64>(p, a, s);
+        case 256128: return chunk_dg<256, 128>(p, a, s);
         default: return cudaErrorInvalidValue;
     }
 }
