@@ -287,16 +287,46 @@ __device__ __forceinline__ long long units_of_group(const Kv4 &p, const Kv4Atten
     }
     return sum * p.H;
 }
+// a / b; most calls' numbers fit 32 bits, whose division is several times shorter.
+__device__ __forceinline__ long long quotient(long long a, long long b) {
+    return ((a | b) >> 32) == 0 ? (long long)((unsigned)a / (unsigned)b) : a / b;
+}
+// The CTA whose range [total * c / grid, total * (c + 1) / grid) has unit u.
 __device__ __forceinline__ long long cta_of(long long u, long long total, long long grid) {
-    long long c = u * grid / total;
-    while (total * c / grid > u) c--;
-    while (total * (c + 1) / grid <= u) c++;
+    long long c = quotient(u * grid, total);
+    while (total * c >= (u + 1) * grid) c--;        // floor(total c / grid) > u
+    while (total * (c + 1) < (u + 1) * grid) c++;   // floor(total (c + 1) / grid) <= u
     return c;
 }
 
 // Partial result of a CTA: [D / 4][rows] of 4 accumulators, then maximum, sum and bits of each row.
 template <int D>
 __host__ __device__ constexpr long long partial_floats() { return (long long)Size<D>::ROWS * (D + 3); }
+
+// Eight columns of O, the c8'th eight, as channels of the row at dst: their order is V's chunks', and within a chunk 0 4
+// 1 5 2 6 3 7. bits: groups that are not finite.
+template <int D, int G, bool BF>
+__device__ __forceinline__ void put_eight(const Kv4Attend &a, uint16_t *dst, int c8, const float *x, float inv, unsigned bits) {
+    constexpr int M = 8 / (D / 64);
+    const int chunk = c8 % 8, d = ((c8 / 8) * M + chunk % M) * (D / 8) + 8 * (chunk / M);
+    const bool nan = (bits >> (d / G)) & 1u;
+    unsigned o[4];
+#pragma unroll
+    for (int e = 0; e < 4; e++) {  // channels 2e, 2e + 1
+        const int c0 = 2 * e < 4 ? 4 * e : 4 * (e - 2) + 1;
+        const float v0 = nan ? __uint_as_float(0x7FC00000u) : x[c0] * inv, v1 = nan ? __uint_as_float(0x7FC00000u) : x[c0 + 2] * inv;
+        o[e] = float_to_bits<BF>(v0) | (float_to_bits<BF>(v1) << 16);
+    }
+    if (a.out_vec16) {
+        *reinterpret_cast<uint4 *>(dst + d) = make_uint4(o[0], o[1], o[2], o[3]);
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            dst[d + 2 * e] = (uint16_t)o[e];
+            dst[d + 2 * e + 1] = (uint16_t)(o[e] >> 16);
+        }
+    }
+}
 
 template <int D, int G, bool BF>
 __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant__ Kv4 p, const __grid_constant__ Kv4Attend a) {
@@ -323,11 +353,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                    o_done = bb + 96, s_free = bb + 112;  // two of each, one s_free
 
     // ---- how much work there is
-    long long sum = 0;
-    for (int b0 = warp * 32; b0 < p.B; b0 += kThreads) sum += units_of_group<D>(p, a, b0, lane, a.status);
+    if (p.B > 32) {  // up to 32 sequences the finder adds up itself
+        long long sum = 0;
+        for (int b0 = warp * 32; b0 < p.B; b0 += kThreads) sum += units_of_group<D>(p, a, b0, lane, a.status);
 #pragma unroll
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-    if (lane == 0) s_sum[warp] = sum;
+        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+        if (lane == 0) s_sum[warp] = sum;
+    }
     if (threadIdx.x == 0) {
         s_stop = 0;
         for (int i = 0; i < 2; i++) {
@@ -434,16 +466,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     } else if (warp > 16) {
         regs_less<kRegsRest>();
         const bool finder = warp == 17;
-        long long total = 0;
-        for (int i = 0; i < kThreads / 32; i++) total += s_sum[i];
-        const long long grid = total < gridDim.x ? total : gridDim.x;  // CTAs that get work
-        const bool idle = blockIdx.x >= grid;
-        long long u = idle ? 0 : total * blockIdx.x / grid;
-        const long long u_end = idle ? 0 : total * (blockIdx.x + 1) / grid;
         int b0 = 0, cur = 0;                     // sequences b0.. of this group, the one in work
         long long before = 0, x = 0, incl = 0;   // units before the group; of each lane's sequence; up to its end
-        auto group = [&]() {
-            x = units_of_group<D>(p, a, b0, lane, nullptr);
+        auto group = [&](int32_t *status) {
+            x = units_of_group<D>(p, a, b0, lane, status);
             incl = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -451,6 +477,16 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                 if (lane >= o) incl += y;
             }
         };
+        if (finder) group(p.B > 32 ? nullptr : a.status);
+        long long total = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        if (p.B > 32) {
+            total = 0;
+            for (int i = 0; i < kThreads / 32; i++) total += s_sum[i];
+        }
+        const long long grid = total < gridDim.x ? total : gridDim.x;  // CTAs that get work
+        const bool idle = blockIdx.x >= grid;
+        long long u = idle ? 0 : quotient(total * blockIdx.x, grid);
+        const long long u_end = idle ? 0 : quotient(total * (blockIdx.x + 1), grid);
         // The description of the segment that begins at u, by the whole warp.
         auto find = [&](Segment &g) {
             if (lane == 0) g.more = u < u_end;
@@ -459,13 +495,13 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             while (!(hit = __ballot_sync(0xFFFFFFFFu, before + incl > u))) {
                 before += __shfl_sync(0xFFFFFFFFu, incl, 31);
                 b0 += 32;
-                group();
+                group(nullptr);
             }
             cur = __ffs(hit) - 1;
             const long long all = __shfl_sync(0xFFFFFFFFu, x, cur), begin = before + __shfl_sync(0xFFFFFFFFu, incl - x, cur);
             const Span s = span_of(p, a, b0 + cur, nullptr);
-            const long long per = all / p.H;
-            int rest = (int)((u - begin) % per);
+            const long long per = quotient(all, p.H), head = quotient(u - begin, per);
+            int rest = (int)(u - begin - head * per);
             int t0 = 0, tiles = 0, pair = 0;
             for (;; pair += 32) {  // 32 pairs at a time
                 const int pairs = (s.n * a.R + ROWS - 1) / ROWS;
@@ -492,7 +528,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             const int here = left < tiles - rest ? (int)left : tiles - rest;
             if (lane == 0) {
                 g.b = b0 + cur;
-                g.kvh = (int)((u - begin) / per);
+                g.kvh = (int)head;
                 g.row0 = pair * ROWS;
                 g.first = s.first;
                 g.n = s.n;
@@ -511,10 +547,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             }
             u += here;
         };
-        if (finder) {
-            group();
-            find(s_segs[0]);
-        }
+        if (finder) find(s_segs[0]);
         for (unsigned round = 0;; round++) {
             __syncthreads();  // (b)
             const Segment &s_seg = s_segs[round & 1];
@@ -527,6 +560,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                     unsigned *tickets = static_cast<unsigned *>(a.ws);
                     __threadfence();
                     const unsigned was = atomicAdd(tickets + s_seg.cta0, 1u);
+                    __threadfence();
                     s_last = was == (unsigned)(s_seg.count - 1);
                     if (s_last) tickets[s_seg.cta0] = 0;
                 }
@@ -953,29 +987,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                     for (int i = 0; i < 32; i++) x[i] = __float_as_uint(__uint_as_float(x[i]) * 128.0f * up);
                     if (whole) {
                         if (mine) {
+                            float y[32];
 #pragma unroll
-                            for (int i = 0; i < 4; i++) {
-                                const int cb = (4 * c + i) / 8, chunk = (4 * c + i) % 8;
-                                const int d = (cb * M + chunk % M) * (D / 8) + 8 * (chunk / M);
-                                unsigned o4[4];
+                            for (int i = 0; i < 32; i++) y[i] = __uint_as_float(x[i]);
 #pragma unroll
-                                for (int e = 0; e < 4; e++) {
-                                    // channels 2e, 2e + 1 of the eight; their columns are in the order 0 4 1 5 2 6 3 7
-                                    const int c0 = 2 * e < 4 ? 4 * e : 4 * (e - 2) + 1, c1 = 2 * e + 1 < 4 ? 4 * e + 2 : 4 * (e - 2) + 3;
-                                    float v0 = __uint_as_float(x[8 * i + c0]) * inv, v1 = __uint_as_float(x[8 * i + c1]) * inv;
-                                    if ((bits >> (d / G)) & 1u) v0 = v1 = __uint_as_float(0x7FC00000u);
-                                    o4[e] = float_to_bits<BF>(v0) | (float_to_bits<BF>(v1) << 16);
-                                }
-                                if (a.out_vec16) {
-                                    *reinterpret_cast<uint4 *>(dst + d) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-                                } else {
-#pragma unroll
-                                    for (int e = 0; e < 4; e++) {
-                                        dst[d + 2 * e] = (uint16_t)o4[e];
-                                        dst[d + 2 * e + 1] = (uint16_t)(o4[e] >> 16);
-                                    }
-                                }
-                            }
+                            for (int i = 0; i < 4; i++) put_eight<D, G, BF>(a, dst, 4 * c + i, y + 8 * i, inv, bits);
                         }
                     } else {
 #pragma unroll
@@ -997,20 +1013,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             }
             n_kv += n_tiles;
             if (s_seg.whole) continue;
-            // ---- an item of several CTAs: the last one joins
-            __threadfence();
+            // ---- an item of several CTAs: the last one joins (the fences are the ticket's thread's, on either side of it)
             __syncthreads();  // (d)
             __syncthreads();  // (e)
             if (s_last && mine) {
-                __threadfence();
                 const int count = s_seg.count, at = q * 128 + r;
                 const long long c0 = s_seg.cta0;
                 auto part_of = [&](int k) { return partials + ((c0 + k) * 2 + (k == 0 ? 1 : 0)) * partial_floats<D>(); };
+                // the parts' maxima and sums; then 32 columns at a time, two parts' loads in flight
                 float top = -INFINITY;
+#pragma unroll 4
                 for (int k = 0; k < count; k++) top = fmaxf(top, __ldcg(part_of(k) + ROWS * D + at));
                 const float base = top == -INFINITY ? 0.0f : top;
                 float l = 0.0f;
                 unsigned bits = 0;
+#pragma unroll 4
                 for (int k = 0; k < count; k++) {
                     const float *tail = part_of(k) + ROWS * D + at;
                     l += __ldcg(tail + ROWS) * ex2(__ldcg(tail) - base);
@@ -1018,25 +1035,23 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                 }
                 const float inv = l == 0.0f ? 0.0f : 1.0f / l;
                 uint16_t *dst = a.out + out_row * a.out_stride + (long long)head * D;
-#pragma unroll 4
-                for (int c8 = 0; c8 < D / 8; c8++) {  // eight columns: eight channels
-                    float x[8];
+#pragma unroll 1
+                for (int c = 0; c < D / 32; c++) {
+                    float x[32];
 #pragma unroll
-                    for (int i = 0; i < 8; i++) x[i] = 0.0f;
+                    for (int i = 0; i < 32; i++) x[i] = 0.0f;
+#pragma unroll 2
                     for (int k = 0; k < count; k++) {
                         const float *src = part_of(k);
                         const float f = ex2(__ldcg(src + ROWS * D + at) - base);
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(src + ((long long)(2 * c8) * ROWS + at) * 4));
-                        const float4 z = __ldcg(reinterpret_cast<const float4 *>(src + ((long long)(2 * c8 + 1) * ROWS + at) * 4));
-                        x[0] += y.x * f, x[1] += y.y * f, x[2] += y.z * f, x[3] += y.w * f;
-                        x[4] += z.x * f, x[5] += z.y * f, x[6] += z.z * f, x[7] += z.w * f;
-                    }
-                    const int cb = c8 / 8, chunk = c8 % 8, d = (cb * M + chunk % M) * (D / 8) + 8 * (chunk / M);
+                        float4 y[8];
 #pragma unroll
-                    for (int i = 0; i < 8; i++) {
-                        const float v = (bits >> (d / G)) & 1u ? __uint_as_float(0x7FC00000u) : x[i] * inv;
-                        dst[d + (i & 1 ? 4 + i / 2 : i / 2)] = (uint16_t)float_to_bits<BF>(v);
+                        for (int i = 0; i < 8; i++) y[i] = __ldcg(reinterpret_cast<const float4 *>(src + ((long long)(8 * c + i) * ROWS + at) * 4));
+#pragma unroll
+                        for (int i = 0; i < 8; i++) x[4 * i] += y[i].x * f, x[4 * i + 1] += y[i].y * f, x[4 * i + 2] += y[i].z * f, x[4 * i + 3] += y[i].w * f;
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; i++) put_eight<D, G, BF>(a, dst, 4 * c + i, x + 8 * i, inv, bits);
                 }
                 if (a.lse) a.lse[out_row * a.Hq + head] = l == 0.0f ? -INFINITY : base * kLn2 + logf(l);
             }
