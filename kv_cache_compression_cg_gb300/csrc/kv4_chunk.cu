@@ -18,7 +18,7 @@
 // minima enter as 16 more channels: m_g against the sum of the row's q over the group, that sum as
 // a high and a low part. So scores are exact up to binary32 sums. V goes in as c s + m with one rounding
 // under a power of two that follows the largest |V^|; weights are rounded to binary16, sums are binary32.
-// A row's maximum is only raised once the scores pass it by 8 (base 2): accumulators are rarely rescaled.
+// A row's maximum is only raised once the scores pass it by kRaise (base 2): accumulators are rarely rescaled.
 //
 // The units of all items (row tile pair x key tile) are dealt out in equal contiguous ranges to one CTA an
 // SM; CTAs that share an item leave partial results, which the last of them joins in order.
@@ -41,6 +41,10 @@ constexpr int kRegsSoftmax = 152, kRegsStore = 72, kRegsRest = 32;  // x 256, 25
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kMaxF = 3.402823466e38f;
 constexpr int kSigMin = -110;
+// Weights are 2^(S - m + kLift), m a running maximum that scores may pass by kRaise: at most 2^15 in binary16, whose
+// normal numbers then reach down to 2^-21 of the largest weight. (Without the lift, weights of long contexts, many below
+// 2^-14 of the largest, added a tenth to the output's error.)
+constexpr float kRaise = 8.0f, kLift = 7.0f;
 constexpr unsigned kWaitLimit = 1u << 20;  // polls of one wait (each up to some microseconds): far above any real one
 
 // ---- PTX -------------------------------------------------------------------
@@ -914,7 +918,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                     for (int i = 0; i < KT; i += 2) t4[(i / 2) & 3] = max3(t4[(i / 2) & 3], __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
                     float top = fmaxf(fmaxf(t4[0], t4[1]), fmaxf(t4[2], t4[3]));
                     top = top == -INFINITY ? top : top * f;
-                    const bool raise = top > m + 8.0f;
+                    const bool raise = top > m + kRaise;
                     if (j > 0) {  // the product before this one has taken P, and O is as it left it
                         wait(o_done + 8 * q, (n_q + j - 1) & 1);
                         fence_after();
@@ -946,7 +950,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                             if (mine && at <= hi && at >= lo && ((held >> (8 * (c / (8 * HALVES)))) & 3u) == 3u) bits |= *(volatile uint8_t *)&s_odd[kv & 3][c];
                         }
                     }
-                    const float base = m == -INFINITY ? 0.0f : m;
+                    const float base = m == -INFINITY ? 0.0f : m - kLift;
                     const uint64_t f2 = pair_of(f, f), b2 = pair_of(-base, -base);
                     uint64_t acc[2] = {0, 0};
 #pragma unroll
@@ -970,6 +974,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                     fence_before();
                     bar_arrive(p_full + 8 * q);
                 }
+                m -= kLift;  // what the weights and their sum are under
                 // ---- results
                 wait(o_done + 8 * q, (n_q + n_tiles - 1) & 1);
                 fence_after();

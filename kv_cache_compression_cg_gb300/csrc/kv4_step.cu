@@ -28,6 +28,10 @@ constexpr int kTile = 32;              // tokens a warp takes at a time: two rec
 // as if they had that many more. Without it CTAs with many short items ended 1.35 times as late as the others.
 constexpr int kItemUnits = 3;
 constexpr int kUnit = kTile * kWarps;  // tokens the work is dealt out in
+// Weights are 2^(S - m + kLift), m a running maximum that scores may pass by kRaise: at most 2^15 in binary16, whose
+// normal numbers then reach down to 2^-23 of the largest weight. (Without the lift, weights of long contexts, many below
+// 2^-14 of the largest, added a tenth to the output's error.)
+constexpr float kRaise = 6.0f, kLift = 9.0f;
 constexpr int kSigMin = -110;            // values below 2^-115 or so lose bits
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 
@@ -457,7 +461,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
         int sig = kSigMin;  // every |m| seen is below 2^sig, every s below 2^(sig - 2): |V^| < 5 2^sig
         float mtop[NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; nt++) mtop[nt][0] = mtop[nt][1] = -INFINITY;  // m + 6
+        for (int nt = 0; nt < NT; nt++) mtop[nt][0] = mtop[nt][1] = -INFINITY;  // m + kRaise
 
         for (int it = 0; it < its; it++) {
             bar_wait(bars + 8 * st, (parity >> st) & 1u, a.status);
@@ -553,7 +557,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                             mm = max_half(mm, mm2[r][k] & 0x7FFF7FFFu);
                         }
                 }
-                // maxima follow in steps of at least 6, sigma in factors of two: as long as no lane's scores or values pass
+                // maxima follow in steps of at least kRaise, sigma in factors of two: as long as no lane's scores or values pass
                 // them by more, nothing is exchanged between lanes and no accumulator is rescaled. Values stay below their
                 // limit while m 2^(-7 - sig) < 2^-7 and 15 s 2^(17 - sig) < 2^17; the test of bit patterns also finds NaNs.
                 const unsigned over = ((ms + 0x08000800u) | (mm + 0x60006000u)) & 0x80008000u;
@@ -616,10 +620,10 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 8));
                             x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, 16));
                             x = x == -INFINITY ? x : x * qscale[nt][c];
-                            const float nm = x > m[nt][c] + 6.0f ? x : m[nt][c];
+                            const float nm = x > m[nt][c] + kRaise ? x : m[nt][c];
                             const float f = m[nt][c] == nm ? 1.0f : exp2_approx(m[nt][c] - nm);
                             m[nt][c] = nm;
-                            mtop[nt][c] = nm + 6.0f;
+                            mtop[nt][c] = nm + kRaise;
                             l[nt][c] *= f;
 #pragma unroll
                             for (int j = 0; j < KS; j++) {
@@ -637,7 +641,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                         float pr[4];
 #pragma unroll
                         for (int c = 0; c < 4; c++) {
-                            const float mm = m[nt][c & 1] == -INFINITY ? 0.0f : m[nt][c & 1];
+                            const float mm = m[nt][c & 1] == -INFINITY ? 0.0f : m[nt][c & 1] - kLift;
                             pr[c] = exp2_approx(fmaf(sc[r][nt][c], qscale[nt][c & 1], -mm));
                             l[nt][c & 1] += pr[c];
                         }
@@ -696,7 +700,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
                     bits[nt][c] |= __shfl_xor_sync(0xFFFFFFFFu, bits[nt][c], x);
                 }
                 if (g == 0) {
-                    s_m[warp][nt * 8 + 2 * t + c] = m[nt][c];
+                    s_m[warp][nt * 8 + 2 * t + c] = m[nt][c] - kLift;  // what weights and sums are under
                     s_l[warp][nt * 8 + 2 * t + c] = l[nt][c];
                     s_bits[warp][nt * 8 + 2 * t + c] = bits[nt][c];
                 }
