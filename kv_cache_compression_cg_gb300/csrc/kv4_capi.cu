@@ -65,10 +65,12 @@ bool strides_ok(const cg_kv4_shape *s, const cg_kv4_batch *b, int32_t n, int64_t
 }
 
 // Which kernels a call of attention takes. A sequence of up to kStepCols (row, query head of a KV head)
-// pairs is the step kernel's, more are the chunk kernel's. With one of each kind both run, on
-// their own sequences; where the average is past the limit the chunk kernel takes them all, which saves the
-// other launch.
-constexpr int kStepCols = 64;
+// pairs is the step kernel's, more are the chunk kernel's. The step kernel reads the keys once for 16 pairs (8 with 256
+// channels), the chunk kernel once for 256 but has some 30 us of fixed cost. With 8 KV heads of 128 channels and 16, 32,
+// 64, 128 pairs: 16 sequences of 4096 keys take 41, 63, 105, 189 us (step) and 74, 75, 78, 84 (chunk), one of 8192 keys 25,
+// 23, 27, 42 and 37, 37, 38, 40. With sequences of both kinds both run, on their own ones; where the average is
+// past the limit the chunk kernel takes them all, which saves the other launch.
+constexpr int kStepCols = 48;
 struct Plan {
     bool step, chunk;
 };

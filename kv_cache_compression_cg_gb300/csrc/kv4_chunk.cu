@@ -257,13 +257,14 @@ __device__ __forceinline__ void tiles_of(const Span &s, const Kv4Attend &a, int 
         tiles = (int)((end + Size<D>::KT - 1) / Size<D>::KT) - t0;
     }
 }
-// Units (key tiles of all pairs, over the KV heads) of sequence b0 + lane. Called by a whole warp; sequences of many
-// pairs are summed by all lanes together.
+// Units (key tiles of all items) of sequence b0 + lane, and its items (pairs x KV heads). Called by a whole warp;
+// sequences of many pairs are summed by all lanes together.
 template <int D>
-__device__ __forceinline__ long long units_of_group(const Kv4 &p, const Kv4Attend &a, int b0, int lane, int32_t *status) {
+__device__ __forceinline__ long long units_of_group(const Kv4 &p, const Kv4Attend &a, int b0, int lane, int32_t *status, long long &items) {
     Span s{0, 0, 0, 0};
     if (b0 + lane < p.B) s = span_of(p, a, b0 + lane, status);
     const int pairs = (s.n * a.R + Size<D>::ROWS - 1) / Size<D>::ROWS;
+    items = (long long)pairs * p.H;
     long long sum = 0;
     int t0, tiles;
     if (__all_sync(0xFFFFFFFFu, pairs <= 4)) {
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     __shared__ uint8_t s_odd[4][KT];  // bits of a token's value groups that are not finite
     __shared__ unsigned s_emax[2][2][8];  // bits of each warp's largest of K, of V
     __shared__ Segment s_segs[2];
-    __shared__ long long s_sum[kThreads / 32];
+    __shared__ long long s_sum[kThreads / 32], s_items[kThreads / 32];
 
     const int warp = __shfl_sync(0xFFFFFFFFu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;  // the shuffle: known to be uniform
     uint8_t *sm = raw + ((1024 - (saddr(raw) & 1023)) & 1023);
@@ -358,11 +359,21 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
 
     // ---- how much work there is
     if (p.B > 32) {  // up to 32 sequences the finder adds up itself
-        long long sum = 0;
-        for (int b0 = warp * 32; b0 < p.B; b0 += kThreads) sum += units_of_group<D>(p, a, b0, lane, a.status);
+        long long sum = 0, items = 0;
+        for (int b0 = warp * 32; b0 < p.B; b0 += kThreads) {
+            long long here;
+            sum += units_of_group<D>(p, a, b0, lane, a.status, here);
+            items += here;
+        }
 #pragma unroll
-        for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-        if (lane == 0) s_sum[warp] = sum;
+        for (int o = 16; o; o >>= 1) {
+            sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
+            items += __shfl_xor_sync(0xFFFFFFFFu, items, o);
+        }
+        if (lane == 0) {
+            s_sum[warp] = sum;
+            s_items[warp] = items;
+        }
     }
     if (threadIdx.x == 0) {
         s_stop = 0;
@@ -472,8 +483,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
         const bool finder = warp == 17;
         int b0 = 0, cur = 0;                     // sequences b0.. of this group, the one in work
         long long before = 0, x = 0, incl = 0;   // units before the group; of each lane's sequence; up to its end
+        long long items = 0;
         auto group = [&](int32_t *status) {
-            x = units_of_group<D>(p, a, b0, lane, status);
+            x = units_of_group<D>(p, a, b0, lane, status, items);
             incl = x;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -484,10 +496,20 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
         if (finder) group(p.B > 32 ? nullptr : a.status);
         long long total = __shfl_sync(0xFFFFFFFFu, incl, 31);
         if (p.B > 32) {
-            total = 0;
-            for (int i = 0; i < kThreads / 32; i++) total += s_sum[i];
+            total = items = 0;
+            for (int i = 0; i < kThreads / 32; i++) {
+                total += s_sum[i];
+                items += s_items[i];
+            }
+        } else {
+#pragma unroll
+            for (int o = 16; o; o >>= 1) items += __shfl_xor_sync(0xFFFFFFFFu, items, o);
         }
-        const long long grid = total < gridDim.x ? total : gridDim.x;  // CTAs that get work
+        // CTAs that get work. Joining a part costs about what a unit does (1 us, by one CTA), so items of few units
+        // are not cut into more parts than units: a CTA has the square root of an item's units at least. (One sequence of
+        // 8192 keys, 8 KV heads, 16 rows: 45 us with 3.4 units each on 152 CTAs.)
+        const int least = max(1, (int)sqrtf((float)total / (float)max(items, 1ll)));
+        const long long grid = max(min(total / least, (long long)gridDim.x), min(total, 1ll));
         const bool idle = blockIdx.x >= grid;
         long long u = idle ? 0 : quotient(total * blockIdx.x, grid);
         const long long u_end = idle ? 0 : quotient(total * (blockIdx.x + 1), grid);
