@@ -146,6 +146,7 @@ cg_status cg_kv4_attention(const uint8_t *pool, const cg_kv4_shape *shape, const
     CG_TRACE_RANGE();
     if (!shape_ok(shape) || !batch_ok(batch) || !layers_ok(shape, layer, 1)) return CG_ERR_INVALID_ARG;
     if (Hq < 1 || Hq % shape->H || Hq > 65536) return CG_ERR_INVALID_ARG;
+    if ((int64_t)batch->rows * Hq > 0x7FFFFFFF) return CG_ERR_INVALID_ARG;
     const int64_t row = (int64_t)Hq * shape->D;
     if (q_row_stride < 0 || out_row_stride < 0 || (batch->rows > 1 && (q_row_stride < row || out_row_stride < row)))
         return CG_ERR_INVALID_ARG;

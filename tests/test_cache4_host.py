@@ -84,6 +84,8 @@ def test_arguments_refused(lib):
     for kw in (dict(pool=None), dict(pool=0x1008), dict(q=None), dict(q=ODD), dict(out=None), dict(ws=None), dict(ws=0x1010),
                dict(Hq=0), dict(Hq=6), dict(Hq=-4), dict(layer=2), dict(layer=-1), dict(qs=1023), dict(os=1023), dict(lse=0x1002)):
         assert attend(lib, s, b, **kw) == 1, kw
+    many = batch(rows=1 << 29, max_rows=1, start=FAKE)
+    assert attend(lib, s, many, Hq=8) == 1  # rows x heads past 2^31
     need = lib.cg_kv4_attention_workspace_bytes(C.byref(s), C.byref(b), 8)
     assert need > 0 and need % 256 == 0
     assert attend(lib, s, b, wsb=need - 1) == 2

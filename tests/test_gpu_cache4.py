@@ -496,3 +496,74 @@ def test_scales_that_are_not_positive(c4, rows, scale):
     out, lse = pr.cache.attend(q, pr.batch(), return_lse=True, scale=scale)
     assert pr.flags() == 0
     check_attention(pr, q, out, lse, scale=scale, sample=60)
+
+
+@pytest.mark.parametrize("rows", [1, 2])
+@pytest.mark.parametrize("B", [33, 700, 1500])
+def test_many_sequences(c4, B, rows):
+    """More sequences than one look at the batch takes, some without rows, lengths from none to a few pages."""
+    rng = np.random.default_rng(B)
+    seqs = [(int(n), int(min(r, n)) if n else 0) for n, r in zip(rng.integers(0, 70, B), rng.integers(0, rows + 1, B))]
+    seqs[0], seqs[-1] = (0, 0), (40, rows)
+    pr = Problem(c4, seqs, P=16, H=1, D=64, group=64, seed=B).fill()
+    q = cuda16(pr.rng.standard_normal((int(pr.start[-1]), 4, 64)).astype(np.float32), pr.dtype)
+    out, lse = pr.cache.attend(q, pr.batch(), return_lse=True)
+    assert pr.flags() == 0
+    check_attention(pr, q, out, lse, sample=300)
+
+
+def test_many_chunks(c4):
+    """The same with chunks: pairs of row tiles over many sequences, long ones between."""
+    rng = np.random.default_rng(7)
+    seqs = [(int(n), int(r)) for n, r in zip(rng.integers(60, 90, 40), rng.integers(20, 60, 40))]
+    seqs[11], seqs[12], seqs[35] = (900, 700), (0, 0), (1400, 260)
+    pr = Problem(c4, seqs, P=48, H=2, D=64, group=32, dtype=torch.bfloat16).fill()
+    q = cuda16(pr.rng.standard_normal((int(pr.start[-1]), 8, 64)).astype(np.float32), pr.dtype)
+    out, lse = pr.cache.attend(q, pr.batch(), return_lse=True)
+    assert pr.flags() == 0
+    check_attention(pr, q, out, lse, sample=300)
+
+
+@pytest.mark.parametrize("D,group", [(64, 64), (128, 32), (256, 128)])
+def test_steps_beside_a_chunk(c4, D, group):
+    """One prompt among many single tokens: either kernel on its own sequences."""
+    seqs = [(200 + i, 1) for i in range(30)] + [(500, 77)] + [(3, 3), (90, 2)]
+    pr = Problem(c4, seqs, P=32, H=1, D=D, group=group, dtype=torch.bfloat16).fill()
+    q = cuda16(pr.rng.standard_normal((int(pr.start[-1]), 4, D)).astype(np.float32), pr.dtype)
+    out, lse = pr.cache.attend(q, pr.batch(), return_lse=True)
+    assert pr.flags() == 0
+    check_attention(pr, q, out, lse, sample=250)
+
+
+@pytest.mark.parametrize("D,group", [(64, 32), (128, 64), (256, 64)])
+@pytest.mark.parametrize("rows", [1, 60, 300])
+def test_one_head_over_a_long_context(c4, D, group, rows):
+    """One KV head: its keys are split over the whole GPU and joined."""
+    pr = Problem(c4, [(12345, rows)], P=64, H=1, D=D, group=group, dtype=torch.float16).fill()
+    q = cuda16(pr.rng.standard_normal((rows, 2, D)).astype(np.float32), pr.dtype)
+    out, lse = pr.cache.attend(q, pr.batch(), return_lse=True)
+    assert pr.flags() == 0
+    check_attention(pr, q, out, lse, sample=24)
+    for _ in range(3):
+        again = pr.cache.attend(q, pr.batch(), return_lse=True)
+        assert torch.equal(again[0], out) and torch.equal(again[1], lse)
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+@pytest.mark.parametrize("pad", [4, 3])
+def test_strided_queries_and_outputs(c4, rows, pad):
+    """Queries sliced out of wider rows, outputs into wider ones; rows that no sequence has stay as they are."""
+    pr = Problem(c4, [(90, rows), (50, rows)], H=2, D=64, group=32, dtype=torch.bfloat16).fill()
+    n = 2 * rows
+    wide = torch.zeros(n + 2, 4 * 64 + pad, dtype=pr.dtype, device="cuda")
+    q = wide[:, pad:].unflatten(1, (4, 64))
+    q.copy_(cuda16(pr.rng.standard_normal((n + 2, 4, 64)).astype(np.float32), pr.dtype))
+    into = torch.full((n + 2, 4 * 64 + pad), 9.0, dtype=pr.dtype, device="cuda")
+    out = into[:, pad:].unflatten(1, (4, 64))
+    b = c4.Batch4(torch.from_numpy(pr.table).cuda(), torch.from_numpy(pr.lens).cuda(), torch.from_numpy(pr.start).cuda(), rows=n + 2, max_rows=rows)
+    pr.cache.attend(q, b, out=out)
+    assert pr.flags() == 0
+    check_attention(pr, q[:n].contiguous(), out[:n].contiguous(), None, sample=100)
+    assert (into[:, :pad] == 9.0).all() and (into[n:] == 9.0).all()
+    plain = pr.cache.attend(q[:n].contiguous(), pr.batch())
+    assert torch.equal(plain, out[:n])
