@@ -567,3 +567,17 @@ def test_strided_queries_and_outputs(c4, rows, pad):
     assert (into[:, :pad] == 9.0).all() and (into[n:] == 9.0).all()
     plain = pr.cache.attend(q[:n].contiguous(), pr.batch())
     assert torch.equal(plain, out[:n])
+
+
+def test_example_serves_from_a_restored_prefix(c4):
+    """compress -> restore -> write into the cache -> decode in a graph. The attention's error against plain attention
+    over the cache's own values: one rounding each of weights, values and output to binary16 (2^-11), all against the
+    weighted mean of |v|, and the scores' and exponentials' 2^-15 (scores up to 30, 8 u each and 2^-19)."""
+    import importlib.util
+    import os
+    at = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "serve_from_prefix.py")
+    spec = importlib.util.spec_from_file_location("serve_from_prefix", at)
+    m = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(m)
+    off = m.serve(layers=2, tokens=300, steps=3, say=lambda *a: None)
+    assert 0.0 < off <= 3 * 2.0 ** -11 + 2.0 ** -15
