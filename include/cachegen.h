@@ -458,7 +458,8 @@ typedef struct cg_kv4_shape {
  * kv_len[b] - 1; kv_len counts them). start == NULL: one row a sequence, rows
  * == B. Device arrays; the host numbers bound them: rows past `rows` and the
  * rows of a sequence with more than max_rows are left out (CG_FLAG_BATCH). Rows
- * that no sequence has (start[B] < rows) are neither read nor written. A row
+ * that no sequence has (start[B] < rows) are not stored, and outputs keep what
+ * they held there. A row
  * at a negative position (more rows than tokens), on a page id outside
  * [0, pages) or past the table is not stored, reads as 0, and is seen by no
  * query; each but the first sets CG_FLAG_BATCH. */

@@ -69,6 +69,7 @@ class Batch4:
             raise ValueError("table, kv_len and start must be on one device")
         self.table, self.kv_len, self.start = table, kv_len, start
         self.rows, self.max_rows = int(rows), int(max_rows)
+        self._device = table.get_device()
         self._c = capi.cg_kv4_batch(B, table.shape[1], self.rows, self.max_rows, table.data_ptr(), kv_len.data_ptr(),
                                     None if start is None else start.data_ptr())
         self._ref = C.byref(self._c)
@@ -138,8 +139,8 @@ class Cache4:
         """Strides (row, layer) of t: [rows, H, D] or [rows, H*D], with a dimension of layers before where there are several."""
         if t.dtype is not self.dtype:
             raise TypeError(f"{name} must be {self.dtype}")
-        if t.get_device() != self._device:
-            raise ValueError(f"{name} must be on the cache's device")
+        if t.get_device() != self._device or batch._device != self._device:
+            raise ValueError(f"{name} and the batch must be on the cache's device")
         shape, stride = t.shape, t.stride()
         n = 0 if layers is None else 1
         if shape[:n + 1] != (batch.rows,) if n == 0 else shape[:2] != (layers, batch.rows):
@@ -175,6 +176,8 @@ class Cache4:
         dtype = self.dtype if dtype is None else dtype
         if dtype not in (self.dtype, torch.float32):
             raise TypeError(f"a read gives {self.dtype} or torch.float32")
+        if batch._device != self._device:
+            raise ValueError("the batch must be on the cache's device")
         shape = (batch.rows, self.H, self.D) if layers is None else (layers, batch.rows, self.H * self.D)
         if out is None:
             if stream is None:
@@ -220,8 +223,8 @@ class Cache4:
         where a row sees nothing)."""
         if q.dtype is not self.dtype:
             raise TypeError(f"q must be {self.dtype}")
-        if q.get_device() != self._device:
-            raise ValueError("q must be on the cache's device")
+        if q.get_device() != self._device or batch._device != self._device:
+            raise ValueError("q and the batch must be on the cache's device")
         D, shape, stride = self.D, q.shape, q.stride()
         if len(shape) != 3 or shape[0] != batch.rows or shape[2] != D or stride[2] != 1 or \
                 (stride[1] != D and shape[1] > 1):

@@ -35,6 +35,14 @@ __device__ __forceinline__ void raise_flag(int32_t *status, int bit) {
     if (status) atomicOr(status, bit);
 }
 
+// Draws a ticket: what the calling thread has seen written (its CTA's writes, after a barrier) is visible to whoever draws
+// a later one, and the other way round.
+__device__ __forceinline__ unsigned draw_ticket(unsigned *ticket) {
+    unsigned was;
+    asm volatile("atom.add.acq_rel.gpu.global.u32 %0, [%1], 1;" : "=r"(was) : "l"(ticket) : "memory");
+    return was;
+}
+
 // Rows of sequence b that the call works on: first row and count, 0 rows where
 // the batch's own bounds leave the sequence out.
 __device__ __forceinline__ void seq_rows(const Kv4 &p, int b, int &first, int &n, int32_t *status) {

@@ -589,10 +589,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
                 __syncthreads();  // (d)
                 if (finder && lane == 0) {
                     unsigned *tickets = static_cast<unsigned *>(a.ws);
-                    __threadfence();
-                    const unsigned was = atomicAdd(tickets + s_seg.cta0, 1u);
-                    __threadfence();
-                    s_last = was == (unsigned)(s_seg.count - 1);
+                    s_last = draw_ticket(tickets + s_seg.cta0) == (unsigned)(s_seg.count - 1);
                     if (s_last) tickets[s_seg.cta0] = 0;
                 }
                 __syncthreads();  // (e)
@@ -1045,7 +1042,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             }
             n_kv += n_tiles;
             if (s_seg.whole) continue;
-            // ---- an item of several CTAs: the last one joins (the fences are the ticket's thread's, on either side of it)
+            // ---- an item of several CTAs: the last one joins
             __syncthreads();  // (d)
             __syncthreads();  // (e)
             if (s_last && mine) {

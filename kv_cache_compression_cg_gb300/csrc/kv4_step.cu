@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
     unsigned parity = 0;  // bit i: of the next wait on stage i
 
     // Items that this CTA shares with others: the one it finds begun, the one it leaves (first_cta < 0: none). Their
-    // tickets are drawn after all its work, with one fence.
+    // tickets are drawn after all its work.
     struct Shared {
         int first_cta, count, first, n, kvh, ct;
     };
@@ -324,10 +324,6 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
             s_at.b = b;
             s_at.before = before;
             s_at.s = s;
-            if (its > 0 && its < s.units) {
-                const int first_cta = (int)cta_of(item_u0, s_at.total, s_at.grid);
-                s_shared[ua == 0] = {first_cta, (int)cta_of(item_u1 - 1, s_at.total, s_at.grid) - first_cta + 1, s.first, s.n, item % p.H, item / p.H};
-            }
         }
         if (its == 0) {
             __syncthreads();
@@ -392,6 +388,10 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
         };
 #pragma unroll
         for (int i = 0; i < ST - 1; i++) issue(i);
+        if (threadIdx.x == 0 && its < s.units) {  // while the copies are on their way
+            const int first_cta = (int)cta_of(item_u0, s_at.total, s_at.grid);
+            s_shared[ua == 0] = {first_cta, (int)cta_of(item_u1 - 1, s_at.total, s_at.grid) - first_cta + 1, s.first, s.n, kvh, ct};
+        }
 
         // ---- queries: under 2^kq of the column's own
         float qsum[NT][NG][2], qscale[NT][2];
@@ -772,19 +772,14 @@ __global__ void __launch_bounds__(kThreads) k_kv4_step(Kv4 p, Kv4Attend a) {
     // ---- shared items: the last CTA to draw an item's ticket joins its parts, in the order of the ranges. The ticket
     // is that of the item's first CTA, which it is the last item of.
     if (s_shared[0].first_cta < 0 && s_shared[1].first_cta < 0) return;
-    if (threadIdx.x == 0) {  // after the barrier: what the whole CTA wrote
-        __threadfence();
+    if (threadIdx.x == 0) {
         int last = 0;
 #pragma unroll
         for (int i = 0; i < 2; i++)
-            if (s_shared[i].first_cta >= 0) {
-                const unsigned was = atomicAdd(tickets + s_shared[i].first_cta, 1u);
-                if (was == (unsigned)(s_shared[i].count - 1)) {
-                    last |= 1 << i;
-                    tickets[s_shared[i].first_cta] = 0;
-                }
+            if (s_shared[i].first_cta >= 0 && draw_ticket(tickets + s_shared[i].first_cta) == (unsigned)(s_shared[i].count - 1)) {
+                last |= 1 << i;
+                tickets[s_shared[i].first_cta] = 0;
             }
-        __threadfence();
         s_last = last;
     }
     __syncthreads();
