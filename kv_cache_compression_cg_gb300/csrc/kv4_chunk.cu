@@ -252,7 +252,7 @@ __device__ __forceinline__ Span span_of(const Kv4 &p, const Kv4Attend &a, int b,
 template <int D>
 __device__ __forceinline__ void tiles_of(const Span &s, const Kv4Attend &a, int pair, int &t0, int &tiles) {
     const int last_row = min((pair + 1) * Size<D>::ROWS, s.n * a.R) - 1;
-    const long long hi = s.pos0 + last_row / a.R, lo = s.pos0 + (long long)pair * Size<D>::ROWS / a.R;
+    const long long hi = s.pos0 + last_row / a.R, lo = s.pos0 + pair * Size<D>::ROWS / a.R;
     const long long end = hi < s.len ? hi + 1 : s.len;  // keys before it are seen by some row
     const long long begin = a.window && lo + 1 > a.window ? lo + 1 - a.window : 0;
     t0 = 0;
@@ -420,71 +420,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
     unsigned n_kv = 0;         // key tiles this CTA has begun: stage and parity of K, V
     unsigned n_q0 = 0, n_q1 = 0;  // tiles of S, P, O of either row tile
 
-    if (warp == 16) {
-        regs_less<kRegsRest>();
-        // ---- matrix instructions
-        unsigned n_s = 0;  // turns of S
-        for (unsigned round = 0;; round++) {
-            __syncthreads();  // (b)
-            const Segment &s_seg = s_segs[round & 1];
-            if (!s_seg.more) break;
-            const int n_tiles = __shfl_sync(0xFFFFFFFFu, s_seg.tiles, 0);
-            const bool two = QT == 2 && __shfl_sync(0xFFFFFFFFu, s_seg.n * a.R - s_seg.row0 > 128, 0);
-            __syncthreads();  // (c)
-            constexpr unsigned id_s = idesc_f16(KT, false), id_o = idesc_f16(D, true);
-            // S is free once the softmax before has it in registers: its turn number n_s
-            auto scores = [&](int i, unsigned kv) {
-                if (n_s > 0) wait(s_free, (n_s - 1) & 1);
-                n_s++;
-                fence_after();
-                if (elected()) {
-                    const unsigned st = kv & 1;
-                    mma_scores<0, D, KT>(tmem, lo128(smb + S::kQ + i * S::kQTile, 16), lo128(smb + S::kK + st * S::kStage, 16), id_s);
-                    mma_ss<0, 0>(tmem, lo_narrow(smb + S::kQN + i * 4096), lo_narrow(smb + S::kKN + st * KT * 32), kHiNarrow, id_s, true);
-                    mma_commit(s_full + 8 * i);
-                    if (i == 1 || !two) mma_commit(k_empty + 8 * st);
-                }
-                __syncwarp();
-            };
-            auto values = [&](int i, unsigned kv, bool add, unsigned par) {
-                wait(p_full + 8 * i, par);
-                fence_after();
-                if (elected()) {
-                    const unsigned st = kv & 1;
-                    mma_values<0, KT>(tmem + kO0 + i * D, tmem + kP0 + i * (KT / 2), lo128(smb + S::kV + st * S::kStage, KT * 128), id_o, add);
-                    mma_commit(o_done + 8 * i);
-                    if (i == 1 || !two) mma_commit(v_empty + 8 * st);
-                }
-                __syncwarp();
-            };
-            unsigned kv = n_kv;
-            wait(k_full + 8 * (kv & 1), (kv >> 1) & 1);
-            scores(0, kv);
-            if (two) scores(1, kv);
-            for (int j = 0; j < n_tiles; j++, kv++) {
-                const bool ahead = j + 1 < n_tiles;
-                if (ahead) {
-                    wait(k_full + 8 * ((kv + 1) & 1), ((kv + 1) >> 1) & 1);
-                    scores(0, kv + 1);
-                }
-                wait(v_full + 8 * (kv & 1), (kv >> 1) & 1);
-                values(0, kv, j > 0, (n_q0 + j) & 1);
-                if (two) {
-                    if (ahead) scores(1, kv + 1);
-                    values(1, kv, j > 0, (n_q1 + j) & 1);
-                }
-            }
-            __syncwarp();
-            n_kv += n_tiles;
-            n_q0 += n_tiles;
-            if (two) n_q1 += n_tiles;
-            if (!s_seg.whole) {
-                __syncthreads();  // (d)
-                __syncthreads();  // (e)
-            }
-        }
-    } else if (warp > 16) {
-        regs_less<kRegsRest>();
+    if (warp >= 16) {
         const bool finder = warp == 17;
         int b0 = 0, cur = 0;                     // sequences b0.. of this group, the one in work
         long long before = 0, x = 0, incl = 0;   // units before the group; of each lane's sequence; up to its end
@@ -579,20 +515,86 @@ __global__ void __launch_bounds__(kThreads, 1) k_kv4_chunk(const __grid_constant
             u += here;
         };
         if (finder) find(s_segs[0]);
-        for (unsigned round = 0;; round++) {
-            __syncthreads();  // (b)
-            const Segment &s_seg = s_segs[round & 1];
-            if (!s_seg.more) break;
-            __syncthreads();  // (c)
-            if (finder) find(s_segs[(round + 1) & 1]);  // while this one is in work
-            if (!s_seg.whole) {
-                __syncthreads();  // (d)
-                if (finder && lane == 0) {
-                    unsigned *tickets = static_cast<unsigned *>(a.ws);
-                    s_last = draw_ticket(tickets + s_seg.cta0) == (unsigned)(s_seg.count - 1);
-                    if (s_last) tickets[s_seg.cta0] = 0;
+        // one instruction for the whole warpgroup; before it, the first search has the launch's registers
+        regs_less<kRegsRest>();
+        if (warp == 16) {
+            // ---- matrix instructions
+            unsigned n_s = 0;  // turns of S
+            for (unsigned round = 0;; round++) {
+                __syncthreads();  // (b)
+                const Segment &s_seg = s_segs[round & 1];
+                if (!s_seg.more) break;
+                const int n_tiles = __shfl_sync(0xFFFFFFFFu, s_seg.tiles, 0);
+                const bool two = QT == 2 && __shfl_sync(0xFFFFFFFFu, s_seg.n * a.R - s_seg.row0 > 128, 0);
+                __syncthreads();  // (c)
+                constexpr unsigned id_s = idesc_f16(KT, false), id_o = idesc_f16(D, true);
+                // S is free once the softmax before has it in registers: its turn number n_s
+                auto scores = [&](int i, unsigned kv) {
+                    if (n_s > 0) wait(s_free, (n_s - 1) & 1);
+                    n_s++;
+                    fence_after();
+                    if (elected()) {
+                        const unsigned st = kv & 1;
+                        mma_scores<0, D, KT>(tmem, lo128(smb + S::kQ + i * S::kQTile, 16), lo128(smb + S::kK + st * S::kStage, 16), id_s);
+                        mma_ss<0, 0>(tmem, lo_narrow(smb + S::kQN + i * 4096), lo_narrow(smb + S::kKN + st * KT * 32), kHiNarrow, id_s, true);
+                        mma_commit(s_full + 8 * i);
+                        if (i == 1 || !two) mma_commit(k_empty + 8 * st);
+                    }
+                    __syncwarp();
+                };
+                auto values = [&](int i, unsigned kv, bool add, unsigned par) {
+                    wait(p_full + 8 * i, par);
+                    fence_after();
+                    if (elected()) {
+                        const unsigned st = kv & 1;
+                        mma_values<0, KT>(tmem + kO0 + i * D, tmem + kP0 + i * (KT / 2), lo128(smb + S::kV + st * S::kStage, KT * 128), id_o, add);
+                        mma_commit(o_done + 8 * i);
+                        if (i == 1 || !two) mma_commit(v_empty + 8 * st);
+                    }
+                    __syncwarp();
+                };
+                unsigned kv = n_kv;
+                wait(k_full + 8 * (kv & 1), (kv >> 1) & 1);
+                scores(0, kv);
+                if (two) scores(1, kv);
+                for (int j = 0; j < n_tiles; j++, kv++) {
+                    const bool ahead = j + 1 < n_tiles;
+                    if (ahead) {
+                        wait(k_full + 8 * ((kv + 1) & 1), ((kv + 1) >> 1) & 1);
+                        scores(0, kv + 1);
+                    }
+                    wait(v_full + 8 * (kv & 1), (kv >> 1) & 1);
+                    values(0, kv, j > 0, (n_q0 + j) & 1);
+                    if (two) {
+                        if (ahead) scores(1, kv + 1);
+                        values(1, kv, j > 0, (n_q1 + j) & 1);
+                    }
                 }
-                __syncthreads();  // (e)
+                __syncwarp();
+                n_kv += n_tiles;
+                n_q0 += n_tiles;
+                if (two) n_q1 += n_tiles;
+                if (!s_seg.whole) {
+                    __syncthreads();  // (d)
+                    __syncthreads();  // (e)
+                }
+            }
+        } else {
+            for (unsigned round = 0;; round++) {
+                __syncthreads();  // (b)
+                const Segment &s_seg = s_segs[round & 1];
+                if (!s_seg.more) break;
+                __syncthreads();  // (c)
+                if (finder) find(s_segs[(round + 1) & 1]);  // while this one is in work
+                if (!s_seg.whole) {
+                    __syncthreads();  // (d)
+                    if (finder && lane == 0) {
+                        unsigned *tickets = static_cast<unsigned *>(a.ws);
+                        s_last = draw_ticket(tickets + s_seg.cta0) == (unsigned)(s_seg.count - 1);
+                        if (s_last) tickets[s_seg.cta0] = 0;
+                    }
+                    __syncthreads();  // (e)
+                }
             }
         }
     } else if (warp >= 8) {
