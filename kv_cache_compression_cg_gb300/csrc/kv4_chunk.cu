@@ -26,7 +26,7 @@
 // 4096 rows over 32768 tokens, 32 query heads over 8 KV heads of 128 channels, binary16: 1.46 to 1.52 ms, 1.36 to 1.41
 // PFLOP/s. The tensor pipe works 63% of the cycles (64 cycles for each of a unit's 34 instructions of 128 x 128 x 16); the
 // schedulers issue in 62%. What is left is the way from S through the softmax's registers back to the next product.
-// 512 rows over 8704 tokens, bfloat16: 90 us, of which the units take 55.
+// 512 rows over 8704 tokens, bfloat16: 88 us, of which the units take 55.
 #include "kv4.cuh"
 
 namespace cg {
